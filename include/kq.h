@@ -292,6 +292,109 @@ kq_status kq_int4_gemm(const uint8_t *xq, int64_t ldxq, const void *sx, int64_t 
  */
 kq_status kq_weight_factor(const void *P, int m, kq_dtype dtype, void *out, void *stream);
 
+/*
+ * kq_rmsnorm_quant -- the residual's addition, the root-mean-square norm and INT8 codes with
+ * a step per row, in one pass: what stands in front of a W8A8 product, or (the normed row) of
+ * a transform plan. Per row t of n values, in fp32:
+ *   1. h = x + residual                       (h = x without a residual)
+ *   2. res_out = h rounded once to x_dtype    (optional; the norm uses the unrounded h)
+ *   3. r = 1 / sqrt(sum(h^2) / n + eps), y = fp32(h * w) * r   (r = 0 where the root is 0)
+ *   4. normed = y rounded once to x_dtype     (optional)
+ *   5. a = max |y|; s32 = fp32(fp32(clip * a) / 127); s = fp16_rne(s32) (or s32);
+ *      q = clamp(rint(fp32(y * fp32(1/s))), -128, 127); s == 0 -> q = 0
+ *      (the quantizer of KQ_FLAG_INT8; optional).
+ *   x          device, T rows of n values of x_dtype (KQ_BF16, KQ_FP16, KQ_FP32), row stride
+ *              ldx elements.
+ *   residual   device, as x with row stride ldr, or NULL.
+ *   w          device, n weights of x_dtype.
+ *   eps        finite, >= 0.    alpha   the clip logit, as in kq_create.
+ *   res_out    device, T rows of n values of x_dtype, row stride ldres, or NULL; may be x or
+ *              residual themselves (same address and stride). NULL without a residual.
+ *   normed     device, T rows of n values of x_dtype, row stride ldy, or NULL; may be x
+ *              itself (same address and stride).
+ *   codes      device, T x n bytes, row stride n, or NULL.
+ *   scales     device, T steps of scale_dtype (KQ_FP16 or KQ_FP32); NULL exactly with codes.
+ * At least one of codes and normed is given. n is 1 .. 65536; rows that are 16-byte aligned
+ * with n a multiple of 8 move 16 bytes at a time, others one value at a time. Outputs may not
+ * overlap each other, nor inputs but as said above. The sum of squares is held in fp32: rows
+ * whose sum is not finite give unspecified outputs (as non-finite inputs do). T == 0 returns
+ * KQ_OK and launches nothing. Asynchronous on `stream`; no allocation. Errors: INVALID_ARG
+ * (NULLs, negative or too small sizes, dtypes, eps, NaN alpha, overlaps), UNSUPPORTED
+ * (n > 65536), ALIGNMENT (a pointer off its type's size), HIP.
+ */
+kq_status kq_rmsnorm_quant(const void *x, int64_t ldx, const void *residual, int64_t ldr,
+                           const void *w, int64_t T, int64_t n, kq_dtype x_dtype, float eps,
+                           float alpha, kq_dtype scale_dtype, void *res_out, int64_t ldres,
+                           void *normed, int64_t ldy, uint8_t *codes, void *scales,
+                           void *stream);
+
+/*
+ * kq_grouped_gemm -- products of codes grouped by expert: kq_int4_gemm's product, INT4 x INT4
+ * or INT8 x INT8, with the rows in E groups of ragged sizes that each have a weight of their
+ * own. Row i of group e (offsets[e] <= i < offsets[e+1]), with source row t = rows[i]:
+ *     out[i][j] = cvt( fp32( fp32( fp32(acc) * sx[t] ) * sw[e][j] ) ),
+ *     acc = sum_k qx[t][k] * qw[e][j][k]  (exact, integer).
+ *   xq       device, T rows of K codes (INT4: two to a byte, the even one in the low nibble;
+ *            INT8: one to a byte), row stride ldxq bytes, as kq_transform_quant and
+ *            kq_rmsnorm_quant write them; 16-byte aligned, ldxq a multiple of 16.
+ *   sx       device, T steps of scale_dtype (KQ_FP16 or KQ_FP32).
+ *   rows     device, R source rows (a row may be named by several groups: a token that
+ *            several experts take), or NULL: row i is source row i, and R is at most T. A row
+ *            outside 0 .. T-1 stands for padding: its output row is left as it was.
+ *   wq       device, E weights of N rows of K codes; expert e's rows start at wq + e * ldwe,
+ *            row stride ldwq bytes; 16-byte aligned, ldwq and ldwe multiples of 16.
+ *   sw       device, E x N steps of scale_dtype, contiguous.
+ *   offsets  device, E + 1 values, not decreasing, in 0 .. R (values outside are taken as the
+ *            nearer end, a decrease as an empty group). Output rows outside every group are
+ *            left as they were.
+ *   bits     4 or 8.
+ *   K        codes per row: K * bits / 8 a multiple of 16 bytes, K at most 65536.
+ *   out      device, R rows of N values of out_dtype (KQ_FP32, KQ_BF16, KQ_FP16), row stride
+ *            ldo elements.
+ * E is 1 .. 4096. R == 0 or N == 0 returns KQ_OK and launches nothing. The call does not read
+ * offsets or rows on the host, so their values may change between replays of a captured
+ * graph. Asynchronous on `stream`; no allocation. Errors: INVALID_ARG (NULLs, sizes, strides
+ * too small, bits, dtypes), UNSUPPORTED (K, E or the grid not as above), ALIGNMENT, HIP.
+ */
+kq_status kq_grouped_gemm(const uint8_t *xq, int64_t ldxq, const void *sx, int64_t T,
+                          const int32_t *rows, int64_t R, const uint8_t *wq, int64_t ldwq,
+                          int64_t ldwe, const void *sw, int64_t N, int64_t K, int64_t E,
+                          const int32_t *offsets, int bits, kq_dtype scale_dtype,
+                          kq_dtype out_dtype, void *out, int64_t ldo, void *stream);
+
+/*
+ * kq_adapter_add -- low-rank adapters of many requests at once, beside a shared projection
+ * (whose output is `base`, from kq_int4_gemm or kq_grouped_gemm): with l = adapter[t],
+ *     out[t] = cvt( base[t] + scaling[l] * B[l] (A[l] x[t]) ),   sums in fp32,
+ * and out[t] = base[t] for a token without an adapter (l outside 0 .. L-1). The low-rank
+ * vector A[l] x[t] stays fp32: the second product takes it as two 16-bit terms whose sum
+ * carries at least 16 bits of it.
+ *   x        device, T rows of K values of dtype (KQ_BF16 or KQ_FP16), row stride ldx
+ *            elements; 16-byte aligned, ldx a multiple of 8.
+ *   A        device, L x r x K of dtype, contiguous, 16-byte aligned.
+ *   B        device, L x N x r of dtype, contiguous, 16-byte aligned.
+ *   adapter  device, T adapter numbers, in any order.
+ *   scaling  device, L fp32 factors, or NULL (all one).
+ *   base     device, T rows of N values of dtype, row stride ldb, or NULL (zeros); 16-byte
+ *            aligned, ldb a multiple of 8.
+ *   out      device, T rows of N values of dtype, row stride ldo, as base; may be base itself
+ *            (same address and stride), but no other input.
+ *   K, N, r  multiples of 8; K and N at most 2^20, r at most 256. L >= 1.
+ *   workspace  device, at least kq_adapter_workspace_size(T, K, r) bytes, 256-byte aligned;
+ *            its contents on entry do not matter. Calls that share a workspace must be
+ *            ordered (same stream), or they race on it.
+ * T == 0 or N == 0 returns KQ_OK and launches nothing. Asynchronous on `stream`; no
+ * allocation; the result does not depend on the order of the sums' parts (no atomics).
+ * Errors: INVALID_ARG (NULLs, sizes, strides too small, dtype, overlaps), UNSUPPORTED
+ * (K, N or r not as above), ALIGNMENT, WORKSPACE, HIP.
+ */
+kq_status kq_adapter_workspace_size(int64_t T, int64_t K, int64_t r, size_t *bytes);
+kq_status kq_adapter_add(const void *x, int64_t ldx, const void *A, const void *B,
+                         const int32_t *adapter, const float *scaling, const void *base,
+                         int64_t ldb, int64_t T, int64_t K, int64_t N, int64_t r, int64_t L,
+                         kq_dtype dtype, void *out, int64_t ldo, void *workspace,
+                         size_t workspace_bytes, void *stream);
+
 /* Free a plan and its device buffers. NULL is a no-op (returns KQ_OK). The caller must
  * make sure no enqueued kq_transform_quant on this plan is still running. */
 kq_status kq_destroy(kq_plan *plan);

@@ -6,9 +6,11 @@ There is no CPU fallback: if libkq.so is missing the first call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
+from typing import Any, NamedTuple
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libkq.so")
@@ -34,7 +36,8 @@ EXPORTS = (
     "kq_choose_factors", "kq_create", "kq_create_ex", "kq_transform_quant", "kq_destroy",
     "kq_plan_clip_ratio", "kq_plan_kernel_name", "kq_plan_kernel_name_for", "kq_status_string",
     "kq_version", "kq_int4_gemm", "kq_workspace_size", "kq_transform_quant_ws",
-    "kq_transform_quant_noalloc", "kq_weight_factor",
+    "kq_transform_quant_noalloc", "kq_weight_factor", "kq_rmsnorm_quant", "kq_grouped_gemm",
+    "kq_adapter_workspace_size", "kq_adapter_add",
 )
 KQ_NOALLOC_SCRATCH_BYTES = 64 << 20
 
@@ -85,6 +88,18 @@ def lib() -> ctypes.CDLL:
     L.kq_int4_gemm.restype = i32
     L.kq_weight_factor.argtypes = [vp, i32, i32, vp, vp]
     L.kq_weight_factor.restype = i32
+    f32, sz = ctypes.c_float, ctypes.c_size_t
+    L.kq_rmsnorm_quant.argtypes = [vp, i64, vp, i64, vp, i64, i64, i32, f32, f32, i32, vp, i64, vp,
+                                   i64, vp, vp, vp]
+    L.kq_rmsnorm_quant.restype = i32
+    L.kq_grouped_gemm.argtypes = [vp, i64, vp, i64, vp, i64, vp, i64, i64, vp, i64, i64, i64, vp,
+                                  i32, i32, i32, vp, i64, vp]
+    L.kq_grouped_gemm.restype = i32
+    L.kq_adapter_workspace_size.argtypes = [i64, i64, i64, ctypes.POINTER(sz)]
+    L.kq_adapter_workspace_size.restype = i32
+    L.kq_adapter_add.argtypes = [vp, i64, vp, vp, vp, vp, vp, i64, i64, i64, i64, i64, i64, i32, vp,
+                                 i64, vp, sz, vp]
+    L.kq_adapter_add.restype = i32
     L.kq_version.argtypes = []
     L.kq_version.restype = i32
     _lib = L
@@ -233,6 +248,230 @@ def int4_gemm(xq, sx, wq, sw, out_dtype="fp32", out=None, stream=None):
         out = torch.empty((T, N), dtype=odt, device=xq.device)
     kq_int4_gemm(xq, xq.stride(0), sx, T, wq, wq.stride(0), sw, N, K, sx.dtype, out_dtype, out,
                  out.stride(0), stream)
+    return out
+
+
+# ------------------------------------------------------------------------------------
+# The operators around a linear layer. Their tensor wrappers check every tensor's type,
+# shape, strides and device before a pointer reaches the C ABI, and run with the tensors'
+# device current, on its current stream or on the one given; what they allocate belongs to
+# that stream.
+def kq_rmsnorm_quant(x, ldx, residual, ldr, w, T, n, x_dtype, eps, alpha, scale_dtype, res_out,
+                     ldres, normed, ldy, codes, scales, stream=None) -> None:
+    st = lib().kq_rmsnorm_quant(_ptr(x), int(ldx), _ptr(residual), int(ldr), _ptr(w), int(T), int(n),
+                                _dtype_code(x_dtype), float(eps), float(alpha),
+                                _dtype_code(scale_dtype), _ptr(res_out), int(ldres), _ptr(normed),
+                                int(ldy), _ptr(codes), _ptr(scales), _stream(stream))
+    _check(st, "kq_rmsnorm_quant")
+
+
+def kq_grouped_gemm(xq, ldxq, sx, T, rows, R, wq, ldwq, ldwe, sw, N, K, E, offsets, bits,
+                    scale_dtype, out_dtype, out, ldo, stream=None) -> None:
+    st = lib().kq_grouped_gemm(_ptr(xq), int(ldxq), _ptr(sx), int(T), _ptr(rows), int(R), _ptr(wq),
+                               int(ldwq), int(ldwe), _ptr(sw), int(N), int(K), int(E), _ptr(offsets),
+                               int(bits), _dtype_code(scale_dtype), _dtype_code(out_dtype), _ptr(out),
+                               int(ldo), _stream(stream))
+    _check(st, "kq_grouped_gemm")
+
+
+def kq_adapter_workspace_size(T: int, K: int, r: int) -> int:
+    b = ctypes.c_size_t(0)
+    _check(lib().kq_adapter_workspace_size(int(T), int(K), int(r), ctypes.byref(b)),
+           "kq_adapter_workspace_size")
+    return int(b.value)
+
+
+def kq_adapter_add(x, ldx, A, B, adapter, scaling, base, ldb, T, K, N, r, L, dtype, out, ldo,
+                   workspace, workspace_bytes, stream=None) -> None:
+    st = lib().kq_adapter_add(_ptr(x), int(ldx), _ptr(A), _ptr(B), _ptr(adapter), _ptr(scaling),
+                              _ptr(base), int(ldb), int(T), int(K), int(N), int(r), int(L),
+                              _dtype_code(dtype), _ptr(out), int(ldo), _ptr(workspace),
+                              int(workspace_bytes), _stream(stream))
+    _check(st, "kq_adapter_add")
+
+
+_HERE_ALREADY = contextlib.nullcontext()
+
+
+@contextlib.contextmanager
+def _elsewhere(device, stream):
+    import torch
+    with torch.cuda.device(device):
+        if stream is None:
+            yield
+        else:
+            if isinstance(stream, int):
+                stream = torch.cuda.ExternalStream(stream, device=device) if stream \
+                    else torch.cuda.default_stream(device)
+            with torch.cuda.stream(stream):
+                yield
+
+
+def _on(device, stream):
+    """Context in which `device` is current and `stream` (None: its current one) takes the
+    launches and owns the allocations."""
+    import torch
+    if stream is None and torch.cuda.current_device() == device.index:
+        return _HERE_ALREADY
+    return _elsewhere(device, stream)
+
+
+def _need(ok, what):
+    if not ok:
+        raise ValueError(what)
+
+
+def _need_rows(name, t, rows, width, dtype, device):
+    """A [rows, width] tensor whose values stand one behind another in each row."""
+    if not (t.dtype == dtype and t.dim() == 2 and t.shape[0] == rows and t.shape[1] == width
+            and t.device == device and (t.stride(1) == 1 or width <= 1)
+            and (t.stride(0) >= width or rows <= 1)):
+        raise ValueError(f"{name} must be a [{rows}, {width}] {dtype} tensor with unit column stride on "
+                         f"{device}")
+
+
+def _need_whole(name, t, shape, dtype, device):
+    if not (t.dtype == dtype and tuple(t.shape) == tuple(shape) and t.device == device
+            and t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
+
+
+def _ld(t, width) -> int:
+    """Row stride; of a single row, whose stride says nothing, its width."""
+    return width if t is None or t.shape[0] <= 1 else t.stride(0)
+
+
+class NormQuant(NamedTuple):
+    """What rmsnorm_quant returns; None for what was not asked for."""
+    codes: Any       # [T, n] uint8: INT8 codes in two's complement
+    scales: Any      # [T] steps
+    residual: Any    # [T, n]: x + residual in x's dtype
+    normed: Any      # [T, n]: the normed rows in x's dtype
+
+
+def rmsnorm_quant(x, weight, residual=None, eps=1e-5, alpha=math.inf, scale_dtype="fp16",
+                  codes=True, normed=False, out=None, stream=None) -> NormQuant:
+    """The residual's addition, the root-mean-square norm and INT8 codes with a step per row
+    (see kq_rmsnorm_quant in include/kq.h).
+
+    x: [T, n] bf16, fp16 or fp32 on the GPU, unit column stride; residual: the same, or None;
+    weight: [n] of x's dtype. codes / normed say which outputs are made. out: a NormQuant of
+    buffers to write instead of new ones (None in it: allocate); out.residual may be x or
+    residual themselves, out.normed may be x itself."""
+    import torch
+    _need(x.dim() == 2 and x.is_cuda, "x must be a [T, n] GPU tensor")
+    T, n = x.shape
+    dev, dt = x.device, x.dtype
+    _need(dt in (torch.bfloat16, torch.float16, torch.float32), "x must be bf16, fp16 or fp32")
+    _need(n >= 1, "x has no columns")
+    _need(codes or normed, "neither codes nor normed rows are asked for")
+    _need_rows("x", x, T, n, dt, dev)
+    _need_whole("weight", weight, (n,), dt, dev)
+    if residual is not None:
+        _need_rows("residual", residual, T, n, dt, dev)
+    sdt = torch.float16 if _dtype_code(scale_dtype) == KQ_FP16 else torch.float32
+    _need(_dtype_code(scale_dtype) != KQ_BF16, "steps are fp16 or fp32")
+    o = out if out is not None else NormQuant(None, None, None, None)
+    with _on(dev, stream):
+        q = s = r = y = None
+        if codes:
+            q = torch.empty((T, n), dtype=torch.uint8, device=dev) if o.codes is None else o.codes
+            s = torch.empty((T,), dtype=sdt, device=dev) if o.scales is None else o.scales
+            if out is not None:
+                _need_whole("out.codes", q, (T, n), torch.uint8, dev)
+                _need_whole("out.scales", s, (T,), sdt, dev)
+        if residual is not None:
+            r = torch.empty((T, n), dtype=dt, device=dev) if o.residual is None else o.residual
+            _need_rows("out.residual", r, T, n, dt, dev)
+        if normed:
+            y = torch.empty((T, n), dtype=dt, device=dev) if o.normed is None else o.normed
+            _need_rows("out.normed", y, T, n, dt, dev)
+        kq_rmsnorm_quant(x, _ld(x, n), residual, _ld(residual, n), weight, T, n, dt, eps, alpha, sdt, r,
+                         _ld(r, n), y, _ld(y, n), q, s)
+    return NormQuant(q, s, r, y)
+
+
+def grouped_gemm(xq, sx, wq, sw, offsets, rows=None, bits=4, out_dtype="fp32", out=None, stream=None):
+    """Products of INT4 or INT8 codes grouped by expert (see kq_grouped_gemm in include/kq.h).
+
+    xq: [T, K bits/8] uint8 codes with steps sx [T]; wq: [E, N, K bits/8] with sw [E, N];
+    offsets: [E + 1] int32, expert e's rows are offsets[e] .. offsets[e+1]-1; rows: [R] int32
+    source row of each (None: row i is xq's row i). Returns out [R, N]; rows outside every
+    group and padding rows (a source row outside xq) are not written, so pass `out` where they
+    have to hold something."""
+    import torch
+    _need(xq.dim() == 2 and xq.is_cuda, "xq must be a [T, bytes] GPU tensor")
+    _need(wq.dim() == 3 and wq.shape[0] >= 1, "wq must be [E, N, bytes]")
+    _need(bits in (4, 8), "bits must be 4 or 8")
+    dev = xq.device
+    T, width = xq.shape
+    E, N, wide = wq.shape
+    _need(width == wide and width >= 1, "xq's and wq's rows of codes differ in length")
+    _need(wq.dtype == torch.uint8 and wq.device == dev and wq.stride(2) == 1,
+          f"wq must be uint8 with unit stride in a row, on {dev}")
+    _need((N <= 1 or wq.stride(1) >= wide) and (E <= 1 or wq.stride(0) >= max(N - 1, 0) * wq.stride(1) + wide),
+          "wq's rows or experts overlap")
+    _need_rows("xq", xq, T, width, torch.uint8, dev)
+    _need(sx.dtype in (torch.float16, torch.float32), "steps are fp16 or fp32")
+    _need_whole("sx", sx, (T,), sx.dtype, dev)
+    _need_whole("sw", sw, (E, N), sx.dtype, dev)
+    _need_whole("offsets", offsets, (E + 1,), torch.int32, dev)
+    R = T
+    if rows is not None:
+        _need(rows.dim() == 1, "rows must be [R] int32")
+        R = rows.shape[0]
+        _need_whole("rows", rows, (R,), torch.int32, dev)
+    odt = {KQ_FP32: torch.float32, KQ_BF16: torch.bfloat16, KQ_FP16: torch.float16}[_dtype_code(out_dtype)]
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty((R, N), dtype=odt, device=dev)
+        else:
+            _need_rows("out", out, R, N, odt, dev)
+        ldw = wide if N <= 1 else wq.stride(1)
+        ldwe = max(N, 1) * ldw if E <= 1 else wq.stride(0)
+        kq_grouped_gemm(xq, _ld(xq, width), sx, T, rows, R, wq, ldw, ldwe, sw, N, width * 8 // bits, E,
+                        offsets, bits, sx.dtype, odt, out, _ld(out, N))
+    return out
+
+
+def adapter_add(x, A, B, adapter, base=None, scaling=None, out=None, workspace=None, stream=None):
+    """Low-rank adapters of many requests beside a shared projection (see kq_adapter_add in
+    include/kq.h): out[t] = base[t] + scaling[l] * B[l] (A[l] x[t]) with l = adapter[t], and
+    base[t] itself where l names no adapter.
+
+    x: [T, K] bf16 or fp16; A: [L, r, K], B: [L, N, r] of x's dtype; adapter: [T] int32;
+    base: [T, N] of x's dtype or None (zeros); scaling: [L] fp32 or None (ones). out may be
+    base itself. workspace: a uint8 tensor of kq_adapter_workspace_size(T, K, r) bytes,
+    allocated here when not given."""
+    import torch
+    _need(x.dim() == 2 and x.is_cuda, "x must be a [T, K] GPU tensor")
+    _need(A.dim() == 3 and B.dim() == 3, "A must be [L, r, K] and B [L, N, r]")
+    dev, dt = x.device, x.dtype
+    _need(dt in (torch.bfloat16, torch.float16), "x must be bf16 or fp16")
+    T, K = x.shape
+    L, r = A.shape[0], A.shape[1]
+    N = B.shape[1]
+    _need_rows("x", x, T, K, dt, dev)
+    _need_whole("A", A, (L, r, K), dt, dev)
+    _need_whole("B", B, (L, N, r), dt, dev)
+    _need_whole("adapter", adapter, (T,), torch.int32, dev)
+    if scaling is not None:
+        _need_whole("scaling", scaling, (L,), torch.float32, dev)
+    if base is not None:
+        _need_rows("base", base, T, N, dt, dev)
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty((T, N), dtype=dt, device=dev)
+        else:
+            _need_rows("out", out, T, N, dt, dev)
+        need = kq_adapter_workspace_size(T, K, r)
+        if workspace is None:
+            workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
+        else:
+            _need(workspace.dtype == torch.uint8 and workspace.device == dev and workspace.is_contiguous()
+                  and workspace.numel() >= need, f"workspace must be {need} contiguous bytes on {dev}")
+        kq_adapter_add(x, _ld(x, K), A, B, adapter, scaling, base, _ld(base, N), T, K, N, r, L, dt, out,
+                       _ld(out, N), workspace, workspace.numel())
     return out
 
 

@@ -21,7 +21,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libkq.so")
 SOURCES = ["kq_api.hip", "kq_fused.hip", "kq_large.hip", "kq_f32.hip", "kq_generic.hip", "kq_gemm.hip",
-           "kq_weight.hip"]
+           "kq_weight.hip", "kq_norm.hip", "kq_grouped.hip", "kq_adapter.hip"]
 ARCH = os.environ.get("KQ_OFFLOAD_ARCH", "gfx950")
 
 HIPCC = shutil.which("hipcc") or "/opt/rocm/bin/hipcc"

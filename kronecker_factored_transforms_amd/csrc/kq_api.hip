@@ -142,9 +142,11 @@ void kq_logf(const char *fmt, ...) {
   fprintf(stderr, "[kq] %s\n", line);
 }
 
+float kq_clip_of_alpha(float alpha) { return clip_from_alpha(alpha); }
+
 extern "C" {
 
-int kq_version(void) { return 10200; }
+int kq_version(void) { return 10300; }
 
 const char *kq_status_string(kq_status s) {
   switch (s) {

@@ -139,3 +139,26 @@ int kq_generic_max_n();
 // error on stderr, prefixed "[kq]". Read once; host code only.
 bool kq_log_on();
 void kq_logf(const char *fmt, ...) __attribute__((format(printf, 1, 2)));
+
+// The clip ratio of a clip logit: sigmoid(alpha) in double, rounded once to fp32 (kq_api.hip).
+float kq_clip_of_alpha(float alpha);
+
+// ---- argument checks: the bytes that a matrix of rows takes up ----
+struct kq_span {
+  uintptr_t lo, hi;      // from its first byte to behind its last; empty for a NULL address
+  uintptr_t ld, width;   // row stride and row length in bytes
+};
+inline kq_span kq_rows_span(const void *p, int64_t rows, int64_t ld, int64_t width, size_t es) {
+  if (!p || rows < 1 || width < 1) return {0, 0, 0, 0};
+  const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+  const uintptr_t l = (uintptr_t)ld * es, w = (uintptr_t)width * es;
+  return {lo, lo + (uintptr_t)(rows - 1) * l + w, l, w};
+}
+// Whether two matrices may share a byte. Column ranges of one wider buffer do not: with the
+// same row stride, the second's rows start in the first's gaps and end before its next row.
+inline bool kq_overlap(const kq_span &a, const kq_span &b) {
+  if (!(a.lo < b.hi && b.lo < a.hi)) return false;
+  if (a.ld != b.ld || a.ld == 0) return true;
+  const uintptr_t d = b.lo >= a.lo ? (b.lo - a.lo) % a.ld : (a.ld - (a.lo - b.lo) % a.ld) % a.ld;
+  return !(d >= a.width && d + b.width <= a.ld);
+}

@@ -1,0 +1,281 @@
+// kq_norm.hip -- the residual's addition, the root-mean-square norm and INT8 codes with a
+// step per row, in one pass over the row.
+//
+//   h = x + residual,  u = h * w,  r = 1 / sqrt(sum(h^2) / n + eps),  y = u * r,
+//   a = max |y|,  s = clip a / 127,  q = clamp(rint(y / s)).
+//
+// r is positive and rounding is monotone, so max |u * r| = (max |u|) * r to the last bit:
+// one reduction over the row, of the pair (sum h^2, max |u|), gives both the norm and the
+// quantizer's step, and the row stays in registers (as u) between them.
+#include "kq_internal.h"
+#include "kq_common.h"
+
+namespace {
+
+constexpr int kMaxRow = 65536;
+
+template <int DT>  // 0: bf16, 1: fp16, 2: fp32
+struct Elem;
+template <>
+struct Elem<0> {
+  typedef uint16_t raw;
+  static __device__ __forceinline__ float get(raw v) { return __uint_as_float((uint32_t)v << 16); }
+  static __device__ __forceinline__ raw put(float v) { return __builtin_bit_cast(uint16_t, (__bf16)v); }
+};
+template <>
+struct Elem<1> {
+  typedef uint16_t raw;
+  static __device__ __forceinline__ float get(raw v) { return (float)__builtin_bit_cast(_Float16, v); }
+  static __device__ __forceinline__ raw put(float v) { return __builtin_bit_cast(uint16_t, (_Float16)v); }
+};
+template <>
+struct Elem<2> {
+  typedef float raw;
+  static __device__ __forceinline__ float get(raw v) { return v; }
+  static __device__ __forceinline__ raw put(float v) { return v; }
+};
+
+// 8 consecutive values at p + i; values from n on read as 0 (not read from memory)
+template <int DT, bool VEC>
+__device__ __forceinline__ void load8(const void *p, int i, int n, float (&v)[8]) {
+  typedef typename Elem<DT>::raw raw;
+  const raw *q = reinterpret_cast<const raw *>(p) + i;
+  if constexpr (VEC) {  // n is a multiple of 8
+    raw t[8];
+    if (i < n) {
+#pragma unroll
+      for (int k = 0; k < (int)sizeof(raw) / 2; ++k)
+        reinterpret_cast<uint4 *>(t)[k] = reinterpret_cast<const uint4 *>(q)[k];
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) t[e] = raw(0);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = Elem<DT>::get(t[e]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = i + e < n ? Elem<DT>::get(q[e]) : 0.f;
+  }
+}
+
+template <int DT, bool VEC>
+__device__ __forceinline__ void store8(void *p, int i, int n, const float (&v)[8]) {
+  typedef typename Elem<DT>::raw raw;
+  raw *q = reinterpret_cast<raw *>(p) + i;
+  if constexpr (VEC) {
+    if (i < n) {
+      raw t[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) t[e] = Elem<DT>::put(v[e]);
+#pragma unroll
+      for (int k = 0; k < (int)sizeof(raw) / 2; ++k)
+        reinterpret_cast<uint4 *>(q)[k] = reinterpret_cast<const uint4 *>(t)[k];
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (i + e < n) q[e] = Elem<DT>::put(v[e]);
+  }
+}
+
+struct NormArgs {
+  const void *x, *res, *w;
+  void *res_out, *normed;
+  uint8_t *codes;
+  void *scales;
+  int64_t T, ldx, ldr, ldres, ldy;
+  int n;
+  float eps, clip;
+  int scale_fp16;
+};
+
+// One row per group of NT threads (a workgroup, or one wave of a workgroup of four); CPT
+// chunks of 8 values per thread.
+template <int DT, int NT, int CPT, bool VEC>
+__global__ __launch_bounds__(NT < 256 ? 256 : NT) void kq_norm_kernel(const NormArgs a) {
+  constexpr int kThreads = NT < 256 ? 256 : NT;
+  constexpr int kRows = kThreads / NT;  // rows per workgroup
+  constexpr int kWaves = NT / 64;       // waves per row
+  typedef typename Elem<DT>::raw raw;
+  __shared__ float s_red[2][2][kThreads / 64];
+  const int tid = threadIdx.x % NT, wave = threadIdx.x / 64;
+  int turn = 0;
+  for (int64_t base = (int64_t)blockIdx.x * kRows; base < a.T; base += (int64_t)gridDim.x * kRows) {
+    const int64_t t = base + threadIdx.x / NT;
+    const bool live = t < a.T;
+    float u[CPT][8];
+    float sum = 0.f, top = 0.f;
+    if (live) {
+      const raw *x = reinterpret_cast<const raw *>(a.x) + t * a.ldx;
+      const raw *r = a.res ? reinterpret_cast<const raw *>(a.res) + t * a.ldr : nullptr;
+      raw *ro = a.res_out ? reinterpret_cast<raw *>(a.res_out) + t * a.ldres : nullptr;
+#pragma unroll
+      for (int c = 0; c < CPT; ++c) {
+        const int i = (c * NT + tid) * 8;
+        float h[8], w[8];
+        load8<DT, VEC>(x, i, a.n, h);
+        if (r) {
+          float v[8];
+          load8<DT, VEC>(r, i, a.n, v);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) h[e] = __fadd_rn(h[e], v[e]);
+        }
+        if (ro) store8<DT, VEC>(ro, i, a.n, h);
+        load8<DT, VEC>(a.w, i, a.n, w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          sum = fmaf(h[e], h[e], sum);
+          u[c][e] = __fmul_rn(h[e], w[e]);
+          top = fmaxf(top, fabsf(u[c][e]));
+        }
+      }
+    }
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) sum += __shfl_xor(sum, o, 64);
+    top = wave_max(top);
+    if constexpr (kWaves > 1) {  // two halves in turn: one barrier per row
+      if (threadIdx.x % 64 == 0) {
+        s_red[turn][0][wave] = sum;
+        s_red[turn][1][wave] = top;
+      }
+      __syncthreads();
+      sum = 0.f;
+      top = 0.f;
+#pragma unroll
+      for (int k = 0; k < kWaves; ++k) {
+        sum += s_red[turn][0][k];
+        top = fmaxf(top, s_red[turn][1][k]);
+      }
+      turn ^= 1;
+    }
+    if (!live) continue;
+    const float root = sqrtf(__fadd_rn(__fdiv_rn(sum, (float)a.n), a.eps));
+    const float rstd = root == 0.f ? 0.f : __fdiv_rn(1.0f, root);
+    const TokenScale ts = token_scale(__fmul_rn(top, rstd), a.clip, a.scale_fp16, 127.0f);
+    if (a.codes && tid == 0) store_scale(a.scales, t, ts, a.scale_fp16);
+    raw *yo = a.normed ? reinterpret_cast<raw *>(a.normed) + t * a.ldy : nullptr;
+    uint8_t *q = a.codes ? a.codes + t * a.n : nullptr;
+#pragma unroll
+    for (int c = 0; c < CPT; ++c) {
+      const int i = (c * NT + tid) * 8;
+      float y[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e] = __fmul_rn(u[c][e], rstd);
+      if (yo) store8<DT, VEC>(yo, i, a.n, y);
+      if (q) {
+        // fp32 y * inv plus 1.5 * 2^23 rounds to the nearest integer, ties to even, into the
+        // low mantissa bits (|y * inv| < 2^22: at most about 127 / clip, else clamped)
+        uint32_t b[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float v = fminf(fmaxf(__fmul_rn(y[e], ts.inv), -128.0f), 127.0f);
+          b[e] = __float_as_uint(__fadd_rn(v, 12582912.0f)) & 0xFFu;
+        }
+        const uint32_t lo = b[0] | b[1] << 8 | b[2] << 16 | b[3] << 24;
+        const uint32_t hi = b[4] | b[5] << 8 | b[6] << 16 | b[7] << 24;
+        if constexpr (VEC) {
+          if (i < a.n) *reinterpret_cast<uint2 *>(q + i) = make_uint2(lo, hi);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (i + e < a.n) q[i + e] = (uint8_t)b[e];
+        }
+      }
+    }
+  }
+}
+
+template <int DT, int NT, int CPT>
+hipError_t launch(const NormArgs &a, bool vec, hipStream_t s) {
+  constexpr int kThreads = NT < 256 ? 256 : NT;
+  constexpr int kRows = kThreads / NT;
+  const int64_t groups = (a.T + kRows - 1) / kRows;
+  const dim3 grid((unsigned)(groups < 16384 ? groups : 16384)), block(kThreads);
+  if (vec)
+    hipLaunchKernelGGL((kq_norm_kernel<DT, NT, CPT, true>), grid, block, 0, s, a);
+  else
+    hipLaunchKernelGGL((kq_norm_kernel<DT, NT, CPT, false>), grid, block, 0, s, a);
+  return hipGetLastError();
+}
+
+template <int DT>
+hipError_t dispatch(const NormArgs &a, bool vec, hipStream_t s) {
+  if (a.n <= 512) return launch<DT, 64, 1>(a, vec, s);
+  if (a.n <= 2048) return launch<DT, 256, 1>(a, vec, s);
+  if (a.n <= 4096) return launch<DT, 256, 2>(a, vec, s);
+  if (a.n <= 8192) return launch<DT, 256, 4>(a, vec, s);
+  if (a.n <= 16384) return launch<DT, 512, 4>(a, vec, s);
+  if (a.n <= 32768) return launch<DT, 1024, 4>(a, vec, s);
+  return launch<DT, 1024, 8>(a, vec, s);
+}
+
+bool off(const void *p, size_t a) { return ((uintptr_t)p % a) != 0; }
+
+}  // namespace
+
+static kq_status rmsnorm_quant_impl(const void *x, int64_t ldx, const void *residual, int64_t ldr,
+                                    const void *w, int64_t T, int64_t n, kq_dtype x_dtype,
+                                    float eps, float alpha, kq_dtype scale_dtype, void *res_out,
+                                    int64_t ldres, void *normed, int64_t ldy, uint8_t *codes,
+                                    void *scales, void *stream) {
+  if (T < 0 || n < 1) return KQ_ERR_INVALID_ARG;
+  if (x_dtype != KQ_BF16 && x_dtype != KQ_FP16 && x_dtype != KQ_FP32) return KQ_ERR_INVALID_ARG;
+  if (scale_dtype != KQ_FP16 && scale_dtype != KQ_FP32) return KQ_ERR_INVALID_ARG;
+  if (!(eps >= 0.f) || !(eps < __builtin_huge_valf()) || alpha != alpha) return KQ_ERR_INVALID_ARG;
+  if (n > kMaxRow) return KQ_ERR_UNSUPPORTED;
+  if (T > ((int64_t)1 << 40) / n) return KQ_ERR_INVALID_ARG;
+  if (T == 0) return KQ_OK;
+  if (!x || !w || (!codes && !normed) || (!codes != !scales)) return KQ_ERR_INVALID_ARG;
+  if (!residual && res_out) return KQ_ERR_INVALID_ARG;
+  if (ldx < n || (residual && ldr < n) || (res_out && ldres < n) || (normed && ldy < n))
+    return KQ_ERR_INVALID_ARG;
+  const int64_t kMaxLd = (int64_t)1 << 40;
+  if (ldx > kMaxLd || ldr > kMaxLd || ldres > kMaxLd || ldy > kMaxLd ||
+      (T > 1 && (double)T * (double)(ldx > ldr ? ldx : ldr) > 4e18))
+    return KQ_ERR_INVALID_ARG;
+  const size_t es = x_dtype == KQ_FP32 ? 4 : 2;
+  if (off(x, es) || off(residual, es) || off(w, es) || off(res_out, es) || off(normed, es) ||
+      off(scales, scale_dtype == KQ_FP32 ? 4 : 2))
+    return KQ_ERR_ALIGNMENT;
+  const kq_span in[3] = {kq_rows_span(x, T, ldx, n, es), kq_rows_span(residual, T, ldr, n, es),
+                         kq_rows_span(w, 1, n, n, es)};
+  const kq_span out[4] = {kq_rows_span(res_out, T, ldres, n, es), kq_rows_span(normed, T, ldy, n, es),
+                          kq_rows_span(codes, T, n, n, 1),
+                          kq_rows_span(scales, 1, T, T, scale_dtype == KQ_FP32 ? 4 : 2)};
+  for (int i = 0; i < 4; ++i) {
+    for (int j = i + 1; j < 4; ++j)
+      if (kq_overlap(out[i], out[j])) return KQ_ERR_INVALID_ARG;
+    for (int j = 0; j < 3; ++j) {
+      if (!kq_overlap(out[i], in[j])) continue;
+      // each thread writes the values it has read: the very same rows may be written in place
+      const bool same = (i == 0 && j == 0 && res_out == x && ldres == ldx) ||
+                        (i == 0 && j == 1 && res_out == residual && ldres == ldr) ||
+                        (i == 1 && j == 0 && normed == x && ldy == ldx);
+      if (!same) return KQ_ERR_INVALID_ARG;
+    }
+  }
+  bool vec = n % 8 == 0 && !off(x, 16) && !off(w, 16) && ldx * es % 16 == 0 && !off(codes, 8);
+  if (residual) vec = vec && !off(residual, 16) && ldr * es % 16 == 0;
+  if (res_out) vec = vec && !off(res_out, 16) && ldres * es % 16 == 0;
+  if (normed) vec = vec && !off(normed, 16) && ldy * es % 16 == 0;
+  const NormArgs a = {x, residual, w, res_out, normed, codes, scales, T, ldx, ldr, ldres, ldy,
+                      (int)n, eps, kq_clip_of_alpha(alpha), scale_dtype == KQ_FP16 ? 1 : 0};
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const hipError_t e = x_dtype == KQ_BF16   ? dispatch<0>(a, vec, s)
+                       : x_dtype == KQ_FP16 ? dispatch<1>(a, vec, s)
+                                            : dispatch<2>(a, vec, s);
+  return e == hipSuccess ? KQ_OK : KQ_ERR_HIP;
+}
+
+extern "C" kq_status kq_rmsnorm_quant(const void *x, int64_t ldx, const void *residual, int64_t ldr,
+                                      const void *w, int64_t T, int64_t n, kq_dtype x_dtype,
+                                      float eps, float alpha, kq_dtype scale_dtype, void *res_out,
+                                      int64_t ldres, void *normed, int64_t ldy, uint8_t *codes,
+                                      void *scales, void *stream) {
+  const kq_status st = rmsnorm_quant_impl(x, ldx, residual, ldr, w, T, n, x_dtype, eps, alpha,
+                                          scale_dtype, res_out, ldres, normed, ldy, codes, scales,
+                                          stream);
+  if (kq_log_on())
+    kq_logf("rmsnorm_quant T=%lld n=%lld: %s", (long long)T, (long long)n, kq_status_string(st));
+  return st;
+}
