@@ -290,9 +290,6 @@ def kq_adapter_add(x, ldx, A, B, adapter, scaling, base, ldb, T, K, N, r, L, dty
     _check(st, "kq_adapter_add")
 
 
-_HERE_ALREADY = contextlib.nullcontext()
-
-
 @contextlib.contextmanager
 def _elsewhere(device, stream):
     import torch
@@ -307,13 +304,22 @@ def _elsewhere(device, stream):
                 yield
 
 
-def _on(device, stream):
-    """Context in which `device` is current and `stream` (None: its current one) takes the
+_HERE_ALREADY = contextlib.nullcontext()
+
+
+def _on(x, stream):
+    """Context in which x's device is current and `stream` (None: its current one) takes the
     launches and owns the allocations."""
     import torch
-    if stream is None and torch.cuda.current_device() == device.index:
+    if stream is None and torch.cuda.current_device() == x.get_device():
         return _HERE_ALREADY
-    return _elsewhere(device, stream)
+    return _elsewhere(x.device, stream)
+
+
+def _current(index) -> int:
+    """Handle of device `index`'s current stream."""
+    import torch
+    return torch._C._cuda_getCurrentRawStream(index)
 
 
 def _need(ok, what):
@@ -321,24 +327,22 @@ def _need(ok, what):
         raise ValueError(what)
 
 
-def _need_rows(name, t, rows, width, dtype, device):
-    """A [rows, width] tensor whose values stand one behind another in each row."""
-    if not (t.dtype == dtype and t.dim() == 2 and t.shape[0] == rows and t.shape[1] == width
-            and t.device == device and (t.stride(1) == 1 or width <= 1)
-            and (t.stride(0) >= width or rows <= 1)):
-        raise ValueError(f"{name} must be a [{rows}, {width}] {dtype} tensor with unit column stride on "
-                         f"{device}")
+def _need_rows(name, t, shape, dtype, index):
+    """A two-dimensional tensor on GPU `index` whose values stand one behind another in each
+    row; returns its row stride (of a single row, whose stride says nothing, its width)."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == index:
+        rows, width = shape
+        ld, step = t.stride()
+        if rows <= 1 and (step == 1 or width <= 1):
+            return width
+        if ld >= width and (step == 1 or width <= 1):
+            return ld
+    raise ValueError(f"{name} must be a {list(shape)} {dtype} tensor with unit column stride on GPU {index}")
 
 
-def _need_whole(name, t, shape, dtype, device):
-    if not (t.dtype == dtype and tuple(t.shape) == tuple(shape) and t.device == device
-            and t.is_contiguous()):
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
-
-
-def _ld(t, width) -> int:
-    """Row stride; of a single row, whose stride says nothing, its width."""
-    return width if t is None or t.shape[0] <= 1 else t.stride(0)
+def _need_whole(name, t, shape, dtype, index):
+    if not (t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {list(shape)} on GPU {index}")
 
 
 class NormQuant(NamedTuple):
@@ -347,6 +351,9 @@ class NormQuant(NamedTuple):
     scales: Any      # [T] steps
     residual: Any    # [T, n]: x + residual in x's dtype
     normed: Any      # [T, n]: the normed rows in x's dtype
+
+
+_ALL_NEW = NormQuant(None, None, None, None)
 
 
 def rmsnorm_quant(x, weight, residual=None, eps=1e-5, alpha=math.inf, scale_dtype="fp16",
@@ -360,34 +367,53 @@ def rmsnorm_quant(x, weight, residual=None, eps=1e-5, alpha=math.inf, scale_dtyp
     residual themselves, out.normed may be x itself."""
     import torch
     _need(x.dim() == 2 and x.is_cuda, "x must be a [T, n] GPU tensor")
-    T, n = x.shape
-    dev, dt = x.device, x.dtype
-    _need(dt in (torch.bfloat16, torch.float16, torch.float32), "x must be bf16, fp16 or fp32")
+    dt, shape, dev = x.dtype, x.shape, x.get_device()
+    T, n = shape
+    dtc = KQ_BF16 if dt is torch.bfloat16 else KQ_FP16 if dt is torch.float16 else KQ_FP32
+    _need(dtc != KQ_FP32 or dt is torch.float32, "x must be bf16, fp16 or fp32")
     _need(n >= 1, "x has no columns")
     _need(codes or normed, "neither codes nor normed rows are asked for")
-    _need_rows("x", x, T, n, dt, dev)
+    sdc = _dtype_code(scale_dtype)
+    _need(sdc == KQ_FP16 or sdc == KQ_FP32, "steps are fp16 or fp32")
+    ldx = _need_rows("x", x, shape, dt, dev)
     _need_whole("weight", weight, (n,), dt, dev)
+    q = s = r = y = None
+    pr = pro = py = pq = ps = None
+    ldr = ldro = ldy = n
     if residual is not None:
-        _need_rows("residual", residual, T, n, dt, dev)
-    sdt = torch.float16 if _dtype_code(scale_dtype) == KQ_FP16 else torch.float32
-    _need(_dtype_code(scale_dtype) != KQ_BF16, "steps are fp16 or fp32")
-    o = out if out is not None else NormQuant(None, None, None, None)
-    with _on(dev, stream):
-        q = s = r = y = None
+        ldr, pr = _need_rows("residual", residual, shape, dt, dev), residual.data_ptr()
+    o = _ALL_NEW if out is None else out
+    with _on(x, stream):
         if codes:
-            q = torch.empty((T, n), dtype=torch.uint8, device=dev) if o.codes is None else o.codes
-            s = torch.empty((T,), dtype=sdt, device=dev) if o.scales is None else o.scales
-            if out is not None:
-                _need_whole("out.codes", q, (T, n), torch.uint8, dev)
+            sdt = torch.float16 if sdc == KQ_FP16 else torch.float32
+            q, s = o.codes, o.scales
+            if q is None:
+                q = x.new_empty(shape, dtype=torch.uint8)
+            else:
+                _need_whole("out.codes", q, shape, torch.uint8, dev)
+            if s is None:
+                s = x.new_empty(T, dtype=sdt)
+            else:
                 _need_whole("out.scales", s, (T,), sdt, dev)
+            pq, ps = q.data_ptr(), s.data_ptr()
         if residual is not None:
-            r = torch.empty((T, n), dtype=dt, device=dev) if o.residual is None else o.residual
-            _need_rows("out.residual", r, T, n, dt, dev)
+            r = o.residual
+            if r is None:
+                r = x.new_empty(shape)
+            else:
+                ldro = _need_rows("out.residual", r, shape, dt, dev)
+            pro = r.data_ptr()
         if normed:
-            y = torch.empty((T, n), dtype=dt, device=dev) if o.normed is None else o.normed
-            _need_rows("out.normed", y, T, n, dt, dev)
-        kq_rmsnorm_quant(x, _ld(x, n), residual, _ld(residual, n), weight, T, n, dt, eps, alpha, sdt, r,
-                         _ld(r, n), y, _ld(y, n), q, s)
+            y = o.normed
+            if y is None:
+                y = x.new_empty(shape)
+            else:
+                ldy = _need_rows("out.normed", y, shape, dt, dev)
+            py = y.data_ptr()
+        st = lib().kq_rmsnorm_quant(x.data_ptr(), ldx, pr, ldr, weight.data_ptr(), T, n, dtc, eps, alpha,
+                                    sdc, pro, ldro, py, ldy, pq, ps, _current(dev))
+    if st != KQ_OK:
+        _check(st, "kq_rmsnorm_quant")
     return NormQuant(q, s, r, y)
 
 
@@ -402,35 +428,44 @@ def grouped_gemm(xq, sx, wq, sw, offsets, rows=None, bits=4, out_dtype="fp32", o
     import torch
     _need(xq.dim() == 2 and xq.is_cuda, "xq must be a [T, bytes] GPU tensor")
     _need(wq.dim() == 3 and wq.shape[0] >= 1, "wq must be [E, N, bytes]")
-    _need(bits in (4, 8), "bits must be 4 or 8")
-    dev = xq.device
+    _need(bits == 4 or bits == 8, "bits must be 4 or 8")
+    dev = xq.get_device()
     T, width = xq.shape
     E, N, wide = wq.shape
     _need(width == wide and width >= 1, "xq's and wq's rows of codes differ in length")
-    _need(wq.dtype == torch.uint8 and wq.device == dev and wq.stride(2) == 1,
-          f"wq must be uint8 with unit stride in a row, on {dev}")
-    _need((N <= 1 or wq.stride(1) >= wide) and (E <= 1 or wq.stride(0) >= max(N - 1, 0) * wq.stride(1) + wide),
-          "wq's rows or experts overlap")
-    _need_rows("xq", xq, T, width, torch.uint8, dev)
-    _need(sx.dtype in (torch.float16, torch.float32), "steps are fp16 or fp32")
-    _need_whole("sx", sx, (T,), sx.dtype, dev)
-    _need_whole("sw", sw, (E, N), sx.dtype, dev)
+    ldx = _need_rows("xq", xq, (T, width), torch.uint8, dev)
+    lde, ldw, step = wq.stride()
+    _need(wq.dtype is torch.uint8 and wq.get_device() == dev and (step == 1 or wide == 1),
+          f"wq must be uint8 with unit stride in a row, on GPU {dev}")
+    if N <= 1:
+        ldw = wide
+    if E <= 1:
+        lde = max(N, 1) * ldw
+    _need(ldw >= wide and lde >= max(N - 1, 0) * ldw + wide, "wq's rows or experts overlap")
+    sdt = sx.dtype
+    _need(sdt is torch.float16 or sdt is torch.float32, "steps are fp16 or fp32")
+    _need_whole("sx", sx, (T,), sdt, dev)
+    _need_whole("sw", sw, (E, N), sdt, dev)
     _need_whole("offsets", offsets, (E + 1,), torch.int32, dev)
-    R = T
+    R, prows = T, None
     if rows is not None:
         _need(rows.dim() == 1, "rows must be [R] int32")
         R = rows.shape[0]
         _need_whole("rows", rows, (R,), torch.int32, dev)
-    odt = {KQ_FP32: torch.float32, KQ_BF16: torch.bfloat16, KQ_FP16: torch.float16}[_dtype_code(out_dtype)]
-    with _on(dev, stream):
+        prows = rows.data_ptr()
+    odc = _dtype_code(out_dtype)
+    odt = torch.bfloat16 if odc == KQ_BF16 else torch.float16 if odc == KQ_FP16 else torch.float32
+    with _on(xq, stream):
         if out is None:
-            out = torch.empty((R, N), dtype=odt, device=dev)
+            out, ldo = sx.new_empty((R, N), dtype=odt), N
         else:
-            _need_rows("out", out, R, N, odt, dev)
-        ldw = wide if N <= 1 else wq.stride(1)
-        ldwe = max(N, 1) * ldw if E <= 1 else wq.stride(0)
-        kq_grouped_gemm(xq, _ld(xq, width), sx, T, rows, R, wq, ldw, ldwe, sw, N, width * 8 // bits, E,
-                        offsets, bits, sx.dtype, odt, out, _ld(out, N))
+            ldo = _need_rows("out", out, (R, N), odt, dev)
+        st = lib().kq_grouped_gemm(xq.data_ptr(), ldx, sx.data_ptr(), T, prows, R, wq.data_ptr(), ldw, lde,
+                                   sw.data_ptr(), N, width * 8 // bits, E, offsets.data_ptr(), bits,
+                                   KQ_FP16 if sdt is torch.float16 else KQ_FP32, odc, out.data_ptr(), ldo,
+                                   _current(dev))
+    if st != KQ_OK:
+        _check(st, "kq_grouped_gemm")
     return out
 
 
@@ -446,32 +481,39 @@ def adapter_add(x, A, B, adapter, base=None, scaling=None, out=None, workspace=N
     import torch
     _need(x.dim() == 2 and x.is_cuda, "x must be a [T, K] GPU tensor")
     _need(A.dim() == 3 and B.dim() == 3, "A must be [L, r, K] and B [L, N, r]")
-    dev, dt = x.device, x.dtype
-    _need(dt in (torch.bfloat16, torch.float16), "x must be bf16 or fp16")
+    dev, dt = x.get_device(), x.dtype
+    _need(dt is torch.bfloat16 or dt is torch.float16, "x must be bf16 or fp16")
     T, K = x.shape
-    L, r = A.shape[0], A.shape[1]
+    L, r, _ = A.shape
     N = B.shape[1]
-    _need_rows("x", x, T, K, dt, dev)
+    ldx = _need_rows("x", x, (T, K), dt, dev)
     _need_whole("A", A, (L, r, K), dt, dev)
     _need_whole("B", B, (L, N, r), dt, dev)
     _need_whole("adapter", adapter, (T,), torch.int32, dev)
+    ps = pb = None
+    ldb = N
     if scaling is not None:
         _need_whole("scaling", scaling, (L,), torch.float32, dev)
+        ps = scaling.data_ptr()
     if base is not None:
-        _need_rows("base", base, T, N, dt, dev)
-    with _on(dev, stream):
+        ldb, pb = _need_rows("base", base, (T, N), dt, dev), base.data_ptr()
+    with _on(x, stream):
         if out is None:
-            out = torch.empty((T, N), dtype=dt, device=dev)
+            out, ldo = x.new_empty((T, N)), N
         else:
-            _need_rows("out", out, T, N, dt, dev)
+            ldo = _need_rows("out", out, (T, N), dt, dev)
         need = kq_adapter_workspace_size(T, K, r)
         if workspace is None:
-            workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
+            workspace = x.new_empty(need, dtype=torch.uint8)
         else:
-            _need(workspace.dtype == torch.uint8 and workspace.device == dev and workspace.is_contiguous()
-                  and workspace.numel() >= need, f"workspace must be {need} contiguous bytes on {dev}")
-        kq_adapter_add(x, _ld(x, K), A, B, adapter, scaling, base, _ld(base, N), T, K, N, r, L, dt, out,
-                       _ld(out, N), workspace, workspace.numel())
+            _need(workspace.dtype is torch.uint8 and workspace.get_device() == dev
+                  and workspace.is_contiguous() and workspace.numel() >= need,
+                  f"workspace must be {need} contiguous bytes on GPU {dev}")
+        st = lib().kq_adapter_add(x.data_ptr(), ldx, A.data_ptr(), B.data_ptr(), adapter.data_ptr(), ps, pb, ldb,
+                                  T, K, N, r, L, KQ_BF16 if dt is torch.bfloat16 else KQ_FP16, out.data_ptr(),
+                                  ldo, workspace.data_ptr(), workspace.numel(), _current(dev))
+    if st != KQ_OK:
+        _check(st, "kq_adapter_add")
     return out
 
 

@@ -7,6 +7,10 @@
 // r is positive and rounding is monotone, so max |u * r| = (max |u|) * r to the last bit:
 // one reduction over the row, of the pair (sum h^2, max |u|), gives both the norm and the
 // quantizer's step, and the row stays in registers (as u) between them.
+//
+// Bound by memory: x and the residual are read once, the sum and the codes written once (7
+// bytes per bf16 value). 16384 x 8192 bf16 with a residual: 163-166 us, 5.7 TB/s, where a
+// device-to-device copy of the same size reaches 5.2.
 #include "kq_internal.h"
 #include "kq_common.h"
 
@@ -35,47 +39,84 @@ struct Elem<2> {
   static __device__ __forceinline__ raw put(float v) { return v; }
 };
 
-// 8 consecutive values at p + i; values from n on read as 0 (not read from memory)
+// 8 consecutive values of a row as they stand in memory
+template <int DT>
+struct Raw8 {
+  typename Elem<DT>::raw v[8];
+};
+
+// The 16-byte words of a chunk. Rows of any alignment are read and written with the same
+// instructions: global memory takes a vector access at any address, and the compiler emits
+// it for a type whose alignment is declared as one element's.
 template <int DT, bool VEC>
-__device__ __forceinline__ void load8(const void *p, int i, int n, float (&v)[8]) {
+struct Words {
+  typedef u32x4_t type;
+};
+template <>
+struct Words<0, false> { typedef u32x4_t type __attribute__((aligned(2))); };
+template <>
+struct Words<1, false> { typedef u32x4_t type __attribute__((aligned(2))); };
+template <>
+struct Words<2, false> { typedef u32x4_t type __attribute__((aligned(4))); };
+
+// Chunk i .. i+7 of a row of n values. VEC: rows are 16-byte aligned and n is a multiple of 8.
+// Otherwise the last chunk may be cut off; its missing values are 0, and never touched.
+template <int DT, bool VEC>
+__device__ __forceinline__ Raw8<DT> load8(const void *p, int i, int n) {
   typedef typename Elem<DT>::raw raw;
+  typedef typename Words<DT, VEC>::type word;
   const raw *q = reinterpret_cast<const raw *>(p) + i;
-  if constexpr (VEC) {  // n is a multiple of 8
-    raw t[8];
-    if (i < n) {
+  Raw8<DT> t = {};
+  if (i + 8 <= n) {
 #pragma unroll
-      for (int k = 0; k < (int)sizeof(raw) / 2; ++k)
-        reinterpret_cast<uint4 *>(t)[k] = reinterpret_cast<const uint4 *>(q)[k];
-    } else {
+    for (int k = 0; k < (int)sizeof(raw) / 2; ++k)
+      reinterpret_cast<u32x4_t *>(t.v)[k] = reinterpret_cast<const word *>(q)[k];
+  } else if constexpr (!VEC) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) t[e] = raw(0);
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = Elem<DT>::get(t[e]);
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = i + e < n ? Elem<DT>::get(q[e]) : 0.f;
+    for (int e = 0; e < 8; ++e)
+      if (i + e < n) t.v[e] = q[e];
   }
+  return t;
 }
 
 template <int DT, bool VEC>
 __device__ __forceinline__ void store8(void *p, int i, int n, const float (&v)[8]) {
   typedef typename Elem<DT>::raw raw;
+  typedef typename Words<DT, VEC>::type word;
   raw *q = reinterpret_cast<raw *>(p) + i;
-  if constexpr (VEC) {
-    if (i < n) {
-      raw t[8];
+  Raw8<DT> t;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) t[e] = Elem<DT>::put(v[e]);
+  for (int e = 0; e < 8; ++e) t.v[e] = Elem<DT>::put(v[e]);
+  if (i + 8 <= n) {
 #pragma unroll
-      for (int k = 0; k < (int)sizeof(raw) / 2; ++k)
-        reinterpret_cast<uint4 *>(q)[k] = reinterpret_cast<const uint4 *>(t)[k];
-    }
-  } else {
+    for (int k = 0; k < (int)sizeof(raw) / 2; ++k)
+      reinterpret_cast<word *>(q)[k] = reinterpret_cast<const u32x4_t *>(t.v)[k];
+  } else if constexpr (!VEC) {
 #pragma unroll
     for (int e = 0; e < 8; ++e)
-      if (i + e < n) q[e] = Elem<DT>::put(v[e]);
+      if (i + e < n) q[e] = t.v[e];
   }
+}
+
+template <bool VEC>
+__device__ __forceinline__ void store_codes(uint8_t *q, int i, int n, uint32_t lo, uint32_t hi) {
+  typedef u32x2_t any __attribute__((aligned(1)));
+  const u32x2_t w = {lo, hi};
+  if (i + 8 <= n) {
+    if constexpr (VEC) *reinterpret_cast<u32x2_t *>(q + i) = w;
+    else *reinterpret_cast<any *>(q + i) = w;
+  } else if constexpr (!VEC) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (i + e < n) q[i + e] = (uint8_t)((e < 4 ? lo >> (8 * e) : hi >> (8 * e - 32)) & 0xFFu);
+  }
+}
+
+// The same value, unknown to the compiler: it would otherwise keep every chunk's offsets and
+// bounds in registers across the rows, and spill u for them.
+__device__ __forceinline__ int opaque(int v) {
+  asm volatile("" : "+v"(v));
+  return v;
 }
 
 struct NormArgs {
@@ -89,50 +130,78 @@ struct NormArgs {
   int scale_fp16;
 };
 
-// One row per group of NT threads (a workgroup, or one wave of a workgroup of four); CPT
-// chunks of 8 values per thread.
+// One row per NT threads (a workgroup, or a wave or half a wave of a workgroup of four waves);
+// CPT chunks of 8 values per thread.
 template <int DT, int NT, int CPT, bool VEC>
-__global__ __launch_bounds__(NT < 256 ? 256 : NT) void kq_norm_kernel(const NormArgs a) {
-  constexpr int kThreads = NT < 256 ? 256 : NT;
+__global__ __launch_bounds__(NT < 128 ? 256 : NT) void kq_norm_kernel(const NormArgs a) {
+  constexpr int kThreads = NT < 128 ? 256 : NT;
   constexpr int kRows = kThreads / NT;  // rows per workgroup
-  constexpr int kWaves = NT / 64;       // waves per row
+  constexpr int kWaves = NT < 64 ? 1 : NT / 64;       // waves per row
+  // a workgroup of 1024 threads has 128 registers for each: there the row comes in parts, and
+  // of its longest rows (n > 32768) a quarter of u waits in LDS, each thread's own values
+  // (2048 rows of 65536: 218 us; all in registers, with spills, 230; half in LDS 252)
+  constexpr int kPart = NT < 1024 || CPT < 2 ? CPT : 2;
+  constexpr int kHeld = CPT < 6 ? CPT : 6;
   typedef typename Elem<DT>::raw raw;
   __shared__ float s_red[2][2][kThreads / 64];
+  __shared__ f32x4 s_u[CPT > kHeld ? (CPT - kHeld) * 2 : 1][CPT > kHeld ? NT : 1];
   const int tid = threadIdx.x % NT, wave = threadIdx.x / 64;
   int turn = 0;
   for (int64_t base = (int64_t)blockIdx.x * kRows; base < a.T; base += (int64_t)gridDim.x * kRows) {
     const int64_t t = base + threadIdx.x / NT;
     const bool live = t < a.T;
-    float u[CPT][8];
+    float u[kHeld][8];
     float sum = 0.f, top = 0.f;
     if (live) {
       const raw *x = reinterpret_cast<const raw *>(a.x) + t * a.ldx;
       const raw *r = a.res ? reinterpret_cast<const raw *>(a.res) + t * a.ldr : nullptr;
       raw *ro = a.res_out ? reinterpret_cast<raw *>(a.res_out) + t * a.ldres : nullptr;
+      // a part of the row is on its way before its first value is used (and before any store,
+      // which the compiler could not move a load across); kPart chunks at a time are held as
+      // they came, beside the u of the whole row
 #pragma unroll
-      for (int c = 0; c < CPT; ++c) {
-        const int i = (c * NT + tid) * 8;
-        float h[8], w[8];
-        load8<DT, VEC>(x, i, a.n, h);
+      for (int c0 = 0; c0 < CPT; c0 += kPart) {
+        const int at = opaque(tid) * 8;
+        Raw8<DT> xv[kPart], rv[kPart], wv[kPart];
+#pragma unroll
+        for (int c = 0; c < kPart; ++c) xv[c] = load8<DT, VEC>(x, (c0 + c) * NT * 8 + at, a.n);
         if (r) {
-          float v[8];
-          load8<DT, VEC>(r, i, a.n, v);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) h[e] = __fadd_rn(h[e], v[e]);
+          for (int c = 0; c < kPart; ++c) rv[c] = load8<DT, VEC>(r, (c0 + c) * NT * 8 + at, a.n);
         }
-        if (ro) store8<DT, VEC>(ro, i, a.n, h);
-        load8<DT, VEC>(a.w, i, a.n, w);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          sum = fmaf(h[e], h[e], sum);
-          u[c][e] = __fmul_rn(h[e], w[e]);
-          top = fmaxf(top, fabsf(u[c][e]));
+        for (int c = 0; c < kPart; ++c) wv[c] = load8<DT, VEC>(a.w, (c0 + c) * NT * 8 + at, a.n);
+#pragma unroll
+        for (int c = 0; c < kPart; ++c) {
+          float h[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            h[e] = Elem<DT>::get(xv[c].v[e]);
+            if (r) h[e] = __fadd_rn(h[e], Elem<DT>::get(rv[c].v[e]));
+          }
+          if (ro) store8<DT, VEC>(ro, (c0 + c) * NT * 8 + at, a.n, h);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            sum = fmaf(h[e], h[e], sum);
+            h[e] = __fmul_rn(h[e], Elem<DT>::get(wv[c].v[e]));
+            top = fmaxf(top, fabsf(h[e]));
+          }
+          if (c0 + c < kHeld) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) u[(c0 + c) % kHeld][e] = h[e];
+          } else {
+            s_u[(c0 + c - kHeld) * 2][tid] = f32x4{h[0], h[1], h[2], h[3]};
+            s_u[(c0 + c - kHeld) * 2 + 1][tid] = f32x4{h[4], h[5], h[6], h[7]};
+          }
         }
+        if constexpr (CPT > kPart) __builtin_amdgcn_sched_barrier(0);
       }
     }
 #pragma unroll
-    for (int o = 32; o >= 1; o >>= 1) sum += __shfl_xor(sum, o, 64);
-    top = wave_max(top);
+    for (int o = (NT < 64 ? NT : 64) / 2; o >= 1; o >>= 1) {
+      sum += __shfl_xor(sum, o, 64);
+      top = fmaxf(top, __shfl_xor(top, o, 64));
+    }
     if constexpr (kWaves > 1) {  // two halves in turn: one barrier per row
       if (threadIdx.x % 64 == 0) {
         s_red[turn][0][wave] = sum;
@@ -157,10 +226,15 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void kq_norm_kernel(const Norm
     uint8_t *q = a.codes ? a.codes + t * a.n : nullptr;
 #pragma unroll
     for (int c = 0; c < CPT; ++c) {
-      const int i = (c * NT + tid) * 8;
+      const int i = c * NT * 8 + opaque(tid) * 8;
       float y[8];
+      if (c < kHeld) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] = __fmul_rn(u[c][e], rstd);
+        for (int e = 0; e < 8; ++e) y[e] = __fmul_rn(u[c % kHeld][e], rstd);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = __fmul_rn(s_u[(c - kHeld) * 2 + e / 4][tid][e % 4], rstd);
+      }
       if (yo) store8<DT, VEC>(yo, i, a.n, y);
       if (q) {
         // fp32 y * inv plus 1.5 * 2^23 rounds to the nearest integer, ties to even, into the
@@ -173,13 +247,7 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void kq_norm_kernel(const Norm
         }
         const uint32_t lo = b[0] | b[1] << 8 | b[2] << 16 | b[3] << 24;
         const uint32_t hi = b[4] | b[5] << 8 | b[6] << 16 | b[7] << 24;
-        if constexpr (VEC) {
-          if (i < a.n) *reinterpret_cast<uint2 *>(q + i) = make_uint2(lo, hi);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (i + e < a.n) q[i + e] = (uint8_t)b[e];
-        }
+        store_codes<VEC>(q, i, a.n, lo, hi);
       }
     }
   }
@@ -187,7 +255,7 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void kq_norm_kernel(const Norm
 
 template <int DT, int NT, int CPT>
 hipError_t launch(const NormArgs &a, bool vec, hipStream_t s) {
-  constexpr int kThreads = NT < 256 ? 256 : NT;
+  constexpr int kThreads = NT < 128 ? 256 : NT;
   constexpr int kRows = kThreads / NT;
   const int64_t groups = (a.T + kRows - 1) / kRows;
   const dim3 grid((unsigned)(groups < 16384 ? groups : 16384)), block(kThreads);
@@ -198,11 +266,23 @@ hipError_t launch(const NormArgs &a, bool vec, hipStream_t s) {
   return hipGetLastError();
 }
 
+// Threads per row by its length: as few as hold it in 2 to 4 chunks each, so that several rows
+// of a compute unit are at different places (reading, reducing, writing). Measured on 16384
+// rows of bf16 with a residual: n = 8192 as 256 x 4 chunks 163-166 us, 512 x 2 174, 1024 x 1 182;
+// n = 2048 as 128 x 2 44 us, 256 x 1 47; n = 1024 as 64 x 2 24.5 us, 64 x 4 27, 256 x 1 32.5;
+// 65536 rows of 256 as 32 lanes 27 us, as 64 (half of them idle) 35. fp32 chunks are twice as
+// large: n = 5120 as 512 x 2 9.4 us, 256 x 4 10.3.
 template <int DT>
 hipError_t dispatch(const NormArgs &a, bool vec, hipStream_t s) {
+  if (a.n <= 256) return launch<DT, 32, 1>(a, vec, s);
   if (a.n <= 512) return launch<DT, 64, 1>(a, vec, s);
-  if (a.n <= 2048) return launch<DT, 256, 1>(a, vec, s);
+  if (a.n <= 1024) return launch<DT, 64, 2>(a, vec, s);
+  if (a.n <= 2048) return launch<DT, 128, 2>(a, vec, s);
   if (a.n <= 4096) return launch<DT, 256, 2>(a, vec, s);
+  if constexpr (DT == 2) {
+    if (a.n <= 8192) return launch<DT, 512, 2>(a, vec, s);
+    if (a.n <= 16384) return launch<DT, 1024, 2>(a, vec, s);
+  }
   if (a.n <= 8192) return launch<DT, 256, 4>(a, vec, s);
   if (a.n <= 16384) return launch<DT, 512, 4>(a, vec, s);
   if (a.n <= 32768) return launch<DT, 1024, 4>(a, vec, s);
