@@ -14,6 +14,7 @@
 namespace {
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
 typedef unsigned int u32x4_t __attribute__((ext_vector_type(4)));
 
 struct GroupedArgs {
@@ -74,6 +75,28 @@ __device__ __forceinline__ void store_out(void *out, int64_t i, float v, int dty
   if (dtype == KQ_FP32) reinterpret_cast<float *>(out)[i] = v;
   else if (dtype == KQ_BF16) reinterpret_cast<__bf16 *>(out)[i] = (__bf16)v;
   else reinterpret_cast<_Float16 *>(out)[i] = (_Float16)v;
+}
+
+// 4 consecutive outputs of a row, of which the first `left` exist; any alignment of the
+// output type (global memory takes a vector access at any address)
+__device__ __forceinline__ void store_out4(void *out, int64_t i, const float (&v)[4], int64_t left,
+                                           int dtype) {
+  typedef u32x4_t any16 __attribute__((aligned(4)));
+  typedef u32x2 any8 __attribute__((aligned(2)));
+  if (left >= 4) {
+    if (dtype == KQ_FP32) {
+      *reinterpret_cast<any16 *>(reinterpret_cast<float *>(out) + i) =
+          u32x4_t{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])};
+    } else if (dtype == KQ_BF16) {
+      const __bf16 h[4] = {(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]};
+      *reinterpret_cast<any8 *>(reinterpret_cast<__bf16 *>(out) + i) = __builtin_bit_cast(u32x2, h);
+    } else {
+      const _Float16 h[4] = {(_Float16)v[0], (_Float16)v[1], (_Float16)v[2], (_Float16)v[3]};
+      *reinterpret_cast<any8 *>(reinterpret_cast<_Float16 *>(out) + i) = __builtin_bit_cast(u32x2, h);
+    }
+  } else {
+    for (int r = 0; r < left; ++r) store_out(out, i + r, v[r], dtype);
+  }
 }
 
 // INT4: a code moved into the high nibble of a byte is the int8 value 16 q, so one dword of 8
@@ -170,8 +193,195 @@ __global__ __launch_bounds__(WAVES * 64) void kq_grouped_stream_kernel(const Gro
     }
 }
 
+// ---- the tile kernel: 256 output channels x up to 256 rows of one group ----
+constexpr int kBM = 256, kBN = 256;
+constexpr int kStep = 128;                       // bytes of a row per step of the reduction
+constexpr int kTileWaves = 8;
+constexpr int kOpBytes = kBM * kStep;            // 32 KiB per operand and buffer
+constexpr int kLoads = kOpBytes / 1024 / kTileWaves;
+static_assert(kBM == kBN && kLoads * 1024 * kTileWaves == kOpBytes, "one layout for both operands");
+
+typedef int i32x16 __attribute__((ext_vector_type(16)));
+
+__device__ __align__(16) const unsigned char kZeros[16] = {};
+
+// 16 int8 operand bytes from one dword pair of INT4 codes (16 codes)
+__device__ __forceinline__ i32x4 unpack16(unsigned x, unsigned y) {
+  constexpr unsigned kHi = 0xF0F0F0F0u;
+  return i32x4{(int)((x << 4) & kHi), (int)(x & kHi), (int)((y << 4) & kHi), (int)(y & kHi)};
+}
+
+// The waves' shares. INT4: 2 x 4 waves of 128 channels x 4 blocks of 16 rows (16x16x64
+// instructions); INT8: 4 x 2 waves of 64 channels x 4 blocks of 32 rows (32x32x32). A wave's
+// blocks stand 64 rows apart, so with NU blocks each the waves cover the first 64 NU rows of
+// the tile and a group's short last tile costs what it holds.
 template <int BITS>
-kq_status launch(const GroupedArgs &a, hipStream_t s) {
+struct Share;
+template <>
+struct Share<4> {
+  static constexpr int kWM = 2, kWN = 4, kSide = 16, kMI = 8;
+  typedef i32x4 acc_t;
+};
+template <>
+struct Share<8> {
+  static constexpr int kWM = 4, kWN = 2, kSide = 32, kMI = 2;
+  typedef i32x16 acc_t;
+};
+
+template <int BITS, int NU>
+__device__ __forceinline__ void tile_product(const GroupedArgs &p, const RowTile &tile, int64_t n0,
+                                             unsigned char (*s_w)[kOpBytes], unsigned char (*s_x)[kOpBytes]) {
+  typedef Share<BITS> S;
+  typedef typename S::acc_t acc_t;
+  constexpr int kRegs = sizeof(acc_t) / 4;
+  static_assert(S::kWN * S::kSide == 64 && S::kWM * S::kWN == kTileWaves, "blocks of a wave: 64 rows apart");
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int g = lane / S::kSide, lr = lane % S::kSide;
+  const int wm = wave % S::kWM, wn = wave / S::kWM;
+
+  // DMA: instruction J = wave kLoads + j of an operand fills tile rows 8 J .. 8 J + 7; lane i
+  // lands at row R = 8 J + i / 8, position i % 8, and reads piece (i % 8) ^ ((R / 2) % 8) of
+  // that row, so that the rows of one fragment read spread over all banks. Rows past the end
+  // of the weight or of the group read a valid row; their products are dropped.
+  const uint8_t *aw[kLoads], *ax[kLoads];
+  const int piece0 = lane % 8;
+#pragma unroll
+  for (int j = 0; j < kLoads; ++j) {
+    const int R = (wave * kLoads + j) * 8 + lane / 8;
+    const int piece = piece0 ^ ((R >> 1) & 7);
+    const int64_t n = n0 + R < p.N ? n0 + R : p.N - 1;
+    aw[j] = p.wq + tile.e * p.ldwe + n * p.ldwq + piece * 16;
+    int64_t t = tile.begin + (R < tile.count ? R : 0);
+    if (p.rows) t = p.rows[t];
+    if (t < 0 || t >= p.T) t = 0;
+    ax[j] = p.xq + t * p.ldxq + piece * 16;
+  }
+  const int steps = (p.pieces + 7) / 8;
+  auto dma_step = [&](int ks, int b) {
+    const int64_t o = (int64_t)ks * kStep;
+    const bool whole = ks * 8 + 8 <= p.pieces;
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j) {
+      // pieces behind the end of a row come from a block of zeros
+      const int R = (wave * kLoads + j) * 8 + lane / 8;
+      const bool in = whole || ks * 8 + (piece0 ^ ((R >> 1) & 7)) < p.pieces;
+      dma16_addr<false>(in ? aw[j] + o : kZeros, lds_addr(s_w[b] + (wave * kLoads + j) * 1024));
+      if ((wave * kLoads + j) * 8 < 64 * NU)
+        dma16_addr<false>(in ? ax[j] + o : kZeros, lds_addr(s_x[b] + (wave * kLoads + j) * 1024));
+    }
+  };
+
+  acc_t acc[S::kMI][NU];
+#pragma unroll
+  for (int m = 0; m < S::kMI; ++m)
+#pragma unroll
+    for (int i = 0; i < NU; ++i)
+#pragma unroll
+      for (int r = 0; r < kRegs; ++r) acc[m][i][r] = 0;
+
+  // rows of this lane's fragments: (R / 2) % 8 is (lr / 2) % 8 for all of them
+  const int sw8 = (lr >> 1) & 7;
+  const int row_w = wm * (kBM / S::kWM) + lr, row_x = wn * S::kSide + lr;
+  dma_step(0, 0);
+  for (int ks = 0; ks < steps; ++ks) {
+    const int b = ks & 1;
+    // this step's tiles have landed, for every wave; every wave is also done reading the
+    // other buffer, which the next DMA overwrites
+    wait_and_fence<kWaitVm0>();
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("" ::: "memory");
+    if (ks + 1 < steps) dma_step(ks + 1, b ^ 1);
+    if constexpr (BITS == 4) {
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {  // 64 bytes (128 codes): two instructions' depth
+        const int off = ((4 * q + g) ^ sw8) * 16;
+        u32x4_t pa[S::kMI], pb[NU];
+#pragma unroll
+        for (int m = 0; m < S::kMI; ++m)
+          pa[m] = *reinterpret_cast<const u32x4_t *>(s_w[b] + (row_w + m * 16) * kStep + off);
+#pragma unroll
+        for (int i = 0; i < NU; ++i)
+          pb[i] = *reinterpret_cast<const u32x4_t *>(s_x[b] + (row_x + i * 64) * kStep + off);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          i32x4 a[S::kMI], bx[NU];
+#pragma unroll
+          for (int m = 0; m < S::kMI; ++m)
+            a[m] = h ? unpack16(pa[m].z, pa[m].w) : unpack16(pa[m].x, pa[m].y);
+#pragma unroll
+          for (int i = 0; i < NU; ++i)
+            bx[i] = h ? unpack16(pb[i].z, pb[i].w) : unpack16(pb[i].x, pb[i].y);
+#pragma unroll
+          for (int m = 0; m < S::kMI; ++m)
+#pragma unroll
+            for (int i = 0; i < NU; ++i)
+              acc[m][i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a[m], bx[i], acc[m][i], 0, 0, 0);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {  // 32 bytes (32 codes)
+        const int off = ((2 * q + g) ^ sw8) * 16;
+        i32x4 pa[S::kMI], pb[NU];
+#pragma unroll
+        for (int m = 0; m < S::kMI; ++m)
+          pa[m] = *reinterpret_cast<const i32x4 *>(s_w[b] + (row_w + m * 32) * kStep + off);
+#pragma unroll
+        for (int i = 0; i < NU; ++i)
+          pb[i] = *reinterpret_cast<const i32x4 *>(s_x[b] + (row_x + i * 64) * kStep + off);
+#pragma unroll
+        for (int m = 0; m < S::kMI; ++m)
+#pragma unroll
+          for (int i = 0; i < NU; ++i)
+            acc[m][i] = __builtin_amdgcn_mfma_i32_32x32x32_i8(pa[m], pb[i], acc[m][i], 0, 0, 0);
+      }
+    }
+    wait_and_fence<kWaitLgkm0>();  // this wave's reads of buffer b have returned
+  }
+
+  // lane: row i * 64 + wn * side + lr; per group of 4 registers 4 consecutive channels
+#pragma unroll
+  for (int i = 0; i < NU; ++i) {
+    const int R = row_x + i * 64;
+    if (R >= tile.count) continue;
+    const int64_t t = p.rows ? (int64_t)p.rows[tile.begin + R] : tile.begin + R;
+    if (t < 0 || t >= p.T) continue;
+    const float sx = load_step(p.sx, t, p.scale_fp16);
+    const int64_t row = (tile.begin + R) * p.ldo;
+#pragma unroll
+    for (int m = 0; m < S::kMI; ++m)
+#pragma unroll
+      for (int r4 = 0; r4 < kRegs; r4 += 4) {
+        const int64_t n = n0 + wm * (kBM / S::kWM) + m * S::kSide + r4 * (64 / S::kSide) + 4 * g;
+        float v[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int sum = BITS == 8 ? acc[m][i][r4 + r] : acc[m][i][r4 + r] >> 8;
+          const float sw = n + r < p.N ? load_step(p.sw, tile.e * p.N + n + r, p.scale_fp16) : 0.f;
+          v[r] = __fmul_rn(__fmul_rn((float)sum, sx), sw);
+        }
+        store_out4(p.out, row + n, v, p.N - n, p.out_dtype);
+      }
+  }
+}
+
+template <int BITS>
+__global__ __launch_bounds__(kTileWaves * 64) void kq_grouped_tile_kernel(const GroupedArgs p, int tiles_m) {
+  __shared__ __align__(16) unsigned char s_w[2][kOpBytes];
+  __shared__ __align__(16) unsigned char s_x[2][kOpBytes];
+  const RowTile tile = find_tile<kBN>(p.offsets, p.E, p.R, (int)(blockIdx.x / tiles_m));
+  if (tile.e < 0) return;
+  const int64_t n0 = (int64_t)(blockIdx.x % tiles_m) * kBM;
+  if (tile.count > 192) tile_product<BITS, 4>(p, tile, n0, s_w, s_x);
+  else if (tile.count > 128) tile_product<BITS, 3>(p, tile, n0, s_w, s_x);
+  else if (tile.count > 64) tile_product<BITS, 2>(p, tile, n0, s_w, s_x);
+  else tile_product<BITS, 1>(p, tile, n0, s_w, s_x);
+}
+
+template <int BITS>
+kq_status launch_stream(const GroupedArgs &a, hipStream_t s) {
   constexpr int MI = 2, NI = 2, WAVES = 4;
   const int64_t tiles_m = (a.N + 16 * MI - 1) / (16 * MI);
   const int64_t tiles = a.R / (16 * NI) + (a.R < a.E ? a.R : a.E);
@@ -179,6 +389,25 @@ kq_status launch(const GroupedArgs &a, hipStream_t s) {
   hipLaunchKernelGGL((kq_grouped_stream_kernel<BITS, MI, NI, WAVES>), dim3((unsigned)(tiles_m * tiles)),
                      dim3(WAVES * 64), 0, s, a, (int)tiles_m);
   return hipGetLastError() == hipSuccess ? KQ_OK : KQ_ERR_HIP;
+}
+
+template <int BITS>
+kq_status launch_tile(const GroupedArgs &a, hipStream_t s) {
+  const int64_t tiles_m = (a.N + kBM - 1) / kBM;
+  const int64_t tiles = a.R / kBN + (a.R < a.E ? a.R : a.E);
+  if (tiles_m * tiles > 0x7FFFFFFF / (kTileWaves * 64)) return KQ_ERR_UNSUPPORTED;
+  hipLaunchKernelGGL(kq_grouped_tile_kernel<BITS>, dim3((unsigned)(tiles_m * tiles)),
+                     dim3(kTileWaves * 64), 0, s, a, (int)tiles_m);
+  return hipGetLastError() == hipSuccess ? KQ_OK : KQ_ERR_HIP;
+}
+
+// Few rows per group: the weights' stream bounds the product; more: the matrix cores do.
+#ifndef GROUPED_CUT
+#define GROUPED_CUT 32
+#endif
+template <int BITS>
+kq_status launch(const GroupedArgs &a, hipStream_t s) {
+  return a.R >= GROUPED_CUT * (int64_t)a.E ? launch_tile<BITS>(a, s) : launch_stream<BITS>(a, s);
 }
 
 constexpr int64_t kMax31 = 0x7FFFFFFF;
