@@ -9,13 +9,12 @@
 // one tile per kTile rows and one more per group, which is as many as ragged ends can make;
 // the workgroups behind the last tile end at once.
 #include "kq_internal.h"
+#include "kq_common.h"
 #include "kq_device.h"
 
 namespace {
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
-typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
-typedef unsigned int u32x4_t __attribute__((ext_vector_type(4)));
 
 struct GroupedArgs {
   const uint8_t *xq, *wq;
@@ -74,28 +73,58 @@ __device__ __forceinline__ float load_step(const void *p, int64_t i, int fp16) {
 __device__ __forceinline__ void store_out(void *out, int64_t i, float v, int dtype) {
   if (dtype == KQ_FP32) reinterpret_cast<float *>(out)[i] = v;
   else if (dtype == KQ_BF16) reinterpret_cast<__bf16 *>(out)[i] = (__bf16)v;
-  else reinterpret_cast<_Float16 *>(out)[i] = (_Float16)v;
+  else reinterpret_cast<_Float16 *>(out)[i] = half_rne(v);
 }
 
 // 4 consecutive outputs of a row, of which the first `left` exist; any alignment of the
 // output type (global memory takes a vector access at any address)
-__device__ __forceinline__ void store_out4(void *out, int64_t i, const float (&v)[4], int64_t left,
-                                           int dtype) {
+template <int OUT>
+__device__ __forceinline__ void store_out4(void *out, int64_t i, const float (&v)[4], int64_t left) {
   typedef u32x4_t any16 __attribute__((aligned(4)));
-  typedef u32x2 any8 __attribute__((aligned(2)));
+  typedef u32x2_t any8 __attribute__((aligned(2)));
   if (left >= 4) {
-    if (dtype == KQ_FP32) {
+    if constexpr (OUT == KQ_FP32) {
       *reinterpret_cast<any16 *>(reinterpret_cast<float *>(out) + i) =
           u32x4_t{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])};
-    } else if (dtype == KQ_BF16) {
+    } else if constexpr (OUT == KQ_BF16) {
       const __bf16 h[4] = {(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]};
-      *reinterpret_cast<any8 *>(reinterpret_cast<__bf16 *>(out) + i) = __builtin_bit_cast(u32x2, h);
+      *reinterpret_cast<any8 *>(reinterpret_cast<__bf16 *>(out) + i) = __builtin_bit_cast(u32x2_t, h);
     } else {
-      const _Float16 h[4] = {(_Float16)v[0], (_Float16)v[1], (_Float16)v[2], (_Float16)v[3]};
-      *reinterpret_cast<any8 *>(reinterpret_cast<_Float16 *>(out) + i) = __builtin_bit_cast(u32x2, h);
+      const _Float16 h[4] = {half_rne(v[0]), half_rne(v[1]), half_rne(v[2]), half_rne(v[3])};
+      *reinterpret_cast<any8 *>(reinterpret_cast<_Float16 *>(out) + i) = __builtin_bit_cast(u32x2_t, h);
     }
   } else {
-    for (int r = 0; r < left; ++r) store_out(out, i + r, v[r], dtype);
+#pragma unroll
+    for (int r = 0; r < 3; ++r)
+      if (r < left) store_out(out, i + r, v[r], OUT);
+  }
+}
+
+// Steps of Q groups of 4 channels, group q from channel n + at(q) on, of a row of N steps that
+// starts at `row`; channels past N get 0 (their outputs are not written).
+template <int Q, typename At>
+__device__ __forceinline__ void load_steps(const void *p, int64_t row, int64_t n, int64_t N, int fp16, At at,
+                                           float (&v)[Q][4]) {
+  typedef u32x4_t any16 __attribute__((aligned(4)));
+  typedef u32x2_t any8 __attribute__((aligned(2)));
+#pragma unroll
+  for (int q = 0; q < Q; ++q) {
+    const int64_t c = n + at(q);
+    if (c + 4 <= N) {
+      if (fp16) {
+        const u32x2_t w = *reinterpret_cast<const any8 *>(reinterpret_cast<const _Float16 *>(p) + row + c);
+        const _Float16 *h = reinterpret_cast<const _Float16 *>(&w);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) v[q][r] = (float)h[r];
+      } else {
+        const u32x4_t w = *reinterpret_cast<const any16 *>(reinterpret_cast<const float *>(p) + row + c);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) v[q][r] = __uint_as_float(w[r]);
+      }
+    } else {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) v[q][r] = c + r < N ? load_step(p, row + c + r, fp16) : 0.f;
+    }
   }
 }
 
@@ -205,6 +234,14 @@ typedef int i32x16 __attribute__((ext_vector_type(16)));
 
 __device__ __align__(16) const unsigned char kZeros[16] = {};
 
+// The same address, in scalar registers (it is the same in every lane)
+__device__ __forceinline__ const uint8_t *uniform(const uint8_t *p) {
+  const uint64_t v = reinterpret_cast<uint64_t>(p);
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v);
+  const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
+  return reinterpret_cast<const uint8_t *>((uint64_t)hi << 32 | lo);
+}
+
 // 16 int8 operand bytes from one dword pair of INT4 codes (16 codes)
 __device__ __forceinline__ i32x4 unpack16(unsigned x, unsigned y) {
   constexpr unsigned kHi = 0xF0F0F0F0u;
@@ -228,7 +265,7 @@ struct Share<8> {
   typedef i32x16 acc_t;
 };
 
-template <int BITS, int NU>
+template <int BITS, int OUT, int NU>
 __device__ __forceinline__ void tile_product(const GroupedArgs &p, const RowTile &tile, int64_t n0,
                                              unsigned char (*s_w)[kOpBytes], unsigned char (*s_x)[kOpBytes]) {
   typedef Share<BITS> S;
@@ -244,14 +281,16 @@ __device__ __forceinline__ void tile_product(const GroupedArgs &p, const RowTile
   // lands at row R = 8 J + i / 8, position i % 8, and reads piece (i % 8) ^ ((R / 2) % 8) of
   // that row, so that the rows of one fragment read spread over all banks. Rows past the end
   // of the weight or of the group read a valid row; their products are dropped.
-  const uint8_t *aw[kLoads], *ax[kLoads];
+  const uint8_t *ax[kLoads];
+  const uint8_t *wbase = uniform(p.wq + tile.e * p.ldwe + n0 * p.ldwq);
+  uint32_t vw[kLoads];  // 256 rows of at most 16 MiB (checked on the host): 32 bits
   const int piece0 = lane % 8;
 #pragma unroll
   for (int j = 0; j < kLoads; ++j) {
     const int R = (wave * kLoads + j) * 8 + lane / 8;
     const int piece = piece0 ^ ((R >> 1) & 7);
-    const int64_t n = n0 + R < p.N ? n0 + R : p.N - 1;
-    aw[j] = p.wq + tile.e * p.ldwe + n * p.ldwq + piece * 16;
+    const int64_t n = n0 + R < p.N ? R : p.N - 1 - n0;
+    vw[j] = (uint32_t)(n * p.ldwq + piece * 16);
     int64_t t = tile.begin + (R < tile.count ? R : 0);
     if (p.rows) t = p.rows[t];
     if (t < 0 || t >= p.T) t = 0;
@@ -259,16 +298,25 @@ __device__ __forceinline__ void tile_product(const GroupedArgs &p, const RowTile
   }
   const int steps = (p.pieces + 7) / 8;
   auto dma_step = [&](int ks, int b) {
-    const int64_t o = (int64_t)ks * kStep;
-    const bool whole = ks * 8 + 8 <= p.pieces;
+    if (ks * 8 + 8 <= p.pieces) {
+      const uint8_t *w = wbase + (int64_t)ks * kStep;
 #pragma unroll
-    for (int j = 0; j < kLoads; ++j) {
-      // pieces behind the end of a row come from a block of zeros
-      const int R = (wave * kLoads + j) * 8 + lane / 8;
-      const bool in = whole || ks * 8 + (piece0 ^ ((R >> 1) & 7)) < p.pieces;
-      dma16_addr<false>(in ? aw[j] + o : kZeros, lds_addr(s_w[b] + (wave * kLoads + j) * 1024));
-      if ((wave * kLoads + j) * 8 < 64 * NU)
-        dma16_addr<false>(in ? ax[j] + o : kZeros, lds_addr(s_x[b] + (wave * kLoads + j) * 1024));
+      for (int j = 0; j < kLoads; ++j) {
+        dma16<false>(w, vw[j], lds_addr(s_w[b] + (wave * kLoads + j) * 1024));
+        if ((wave * kLoads + j) * 8 < 64 * NU)
+          dma16_addr<false>(ax[j], lds_addr(s_x[b] + (wave * kLoads + j) * 1024));
+        ax[j] += kStep;
+      }
+    } else {  // the last step of a row that ends inside it: the rest comes from a block of zeros
+#pragma unroll
+      for (int j = 0; j < kLoads; ++j) {
+        const int R = (wave * kLoads + j) * 8 + lane / 8;
+        const bool in = ks * 8 + (piece0 ^ ((R >> 1) & 7)) < p.pieces;
+        dma16_addr<false>(in ? wbase + (int64_t)ks * kStep + vw[j] : kZeros,
+                          lds_addr(s_w[b] + (wave * kLoads + j) * 1024));
+        if ((wave * kLoads + j) * 8 < 64 * NU)
+          dma16_addr<false>(in ? ax[j] : kZeros, lds_addr(s_x[b] + (wave * kLoads + j) * 1024));
+      }
     }
   };
 
@@ -341,7 +389,13 @@ __device__ __forceinline__ void tile_product(const GroupedArgs &p, const RowTile
     wait_and_fence<kWaitLgkm0>();  // this wave's reads of buffer b have returned
   }
 
-  // lane: row i * 64 + wn * side + lr; per group of 4 registers 4 consecutive channels
+  // lane: row i * 64 + wn * side + lr; per group of 4 registers 4 consecutive channels. The
+  // channels' steps first, then row by row.
+  constexpr int kQ = S::kMI * kRegs / 4;  // groups of 4 channels
+  const int64_t nl = n0 + wm * (kBM / S::kWM) + 4 * g;  // group q: nl + group_at(q)
+  auto group_at = [](int q) { return q / (kRegs / 4) * S::kSide + q % (kRegs / 4) * 4 * (64 / S::kSide); };
+  float sw[kQ][4];
+  load_steps<kQ>(p.sw, tile.e * p.N, nl, p.N, p.scale_fp16, group_at, sw);
 #pragma unroll
   for (int i = 0; i < NU; ++i) {
     const int R = row_x + i * 64;
@@ -349,35 +403,31 @@ __device__ __forceinline__ void tile_product(const GroupedArgs &p, const RowTile
     const int64_t t = p.rows ? (int64_t)p.rows[tile.begin + R] : tile.begin + R;
     if (t < 0 || t >= p.T) continue;
     const float sx = load_step(p.sx, t, p.scale_fp16);
-    const int64_t row = (tile.begin + R) * p.ldo;
+    const int64_t row = (tile.begin + R) * p.ldo + nl;
 #pragma unroll
-    for (int m = 0; m < S::kMI; ++m)
+    for (int q = 0; q < kQ; ++q) {
+      float v[4];
 #pragma unroll
-      for (int r4 = 0; r4 < kRegs; r4 += 4) {
-        const int64_t n = n0 + wm * (kBM / S::kWM) + m * S::kSide + r4 * (64 / S::kSide) + 4 * g;
-        float v[4];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int sum = BITS == 8 ? acc[m][i][r4 + r] : acc[m][i][r4 + r] >> 8;
-          const float sw = n + r < p.N ? load_step(p.sw, tile.e * p.N + n + r, p.scale_fp16) : 0.f;
-          v[r] = __fmul_rn(__fmul_rn((float)sum, sx), sw);
-        }
-        store_out4(p.out, row + n, v, p.N - n, p.out_dtype);
+      for (int r = 0; r < 4; ++r) {
+        const int a = acc[q / (kRegs / 4)][i][q % (kRegs / 4) * 4 + r];
+        v[r] = __fmul_rn(__fmul_rn((float)(BITS == 8 ? a : a >> 8), sx), sw[q][r]);
       }
+      store_out4<OUT>(p.out, row + group_at(q), v, p.N - nl - group_at(q));
+    }
   }
 }
 
-template <int BITS>
+template <int BITS, int OUT>
 __global__ __launch_bounds__(kTileWaves * 64) void kq_grouped_tile_kernel(const GroupedArgs p, int tiles_m) {
   __shared__ __align__(16) unsigned char s_w[2][kOpBytes];
   __shared__ __align__(16) unsigned char s_x[2][kOpBytes];
   const RowTile tile = find_tile<kBN>(p.offsets, p.E, p.R, (int)(blockIdx.x / tiles_m));
   if (tile.e < 0) return;
   const int64_t n0 = (int64_t)(blockIdx.x % tiles_m) * kBM;
-  if (tile.count > 192) tile_product<BITS, 4>(p, tile, n0, s_w, s_x);
-  else if (tile.count > 128) tile_product<BITS, 3>(p, tile, n0, s_w, s_x);
-  else if (tile.count > 64) tile_product<BITS, 2>(p, tile, n0, s_w, s_x);
-  else tile_product<BITS, 1>(p, tile, n0, s_w, s_x);
+  if (tile.count > 192) tile_product<BITS, OUT, 4>(p, tile, n0, s_w, s_x);
+  else if (tile.count > 128) tile_product<BITS, OUT, 3>(p, tile, n0, s_w, s_x);
+  else if (tile.count > 64) tile_product<BITS, OUT, 2>(p, tile, n0, s_w, s_x);
+  else tile_product<BITS, OUT, 1>(p, tile, n0, s_w, s_x);
 }
 
 template <int BITS>
@@ -396,8 +446,13 @@ kq_status launch_tile(const GroupedArgs &a, hipStream_t s) {
   const int64_t tiles_m = (a.N + kBM - 1) / kBM;
   const int64_t tiles = a.R / kBN + (a.R < a.E ? a.R : a.E);
   if (tiles_m * tiles > 0x7FFFFFFF / (kTileWaves * 64)) return KQ_ERR_UNSUPPORTED;
-  hipLaunchKernelGGL(kq_grouped_tile_kernel<BITS>, dim3((unsigned)(tiles_m * tiles)),
-                     dim3(kTileWaves * 64), 0, s, a, (int)tiles_m);
+  const dim3 grid((unsigned)(tiles_m * tiles)), block(kTileWaves * 64);
+  if (a.out_dtype == KQ_FP32)
+    hipLaunchKernelGGL((kq_grouped_tile_kernel<BITS, KQ_FP32>), grid, block, 0, s, a, (int)tiles_m);
+  else if (a.out_dtype == KQ_BF16)
+    hipLaunchKernelGGL((kq_grouped_tile_kernel<BITS, KQ_BF16>), grid, block, 0, s, a, (int)tiles_m);
+  else
+    hipLaunchKernelGGL((kq_grouped_tile_kernel<BITS, KQ_FP16>), grid, block, 0, s, a, (int)tiles_m);
   return hipGetLastError() == hipSuccess ? KQ_OK : KQ_ERR_HIP;
 }
 
@@ -411,6 +466,7 @@ kq_status launch(const GroupedArgs &a, hipStream_t s) {
 }
 
 constexpr int64_t kMax31 = 0x7FFFFFFF;
+constexpr int64_t kMaxLdw = (1 << 24) - 256;  // 256 rows within 32 bits of offset
 
 bool off(const void *p, size_t a) { return ((uintptr_t)p % a) != 0; }
 
@@ -435,7 +491,7 @@ static kq_status grouped_gemm_impl(const uint8_t *xq, int64_t ldxq, const void *
   const int64_t rb = K * bits / 8;
   if (ldxq < rb || ldwq < rb || ldo < N) return KQ_ERR_INVALID_ARG;
   // no product of a row and a stride passes 2^62
-  if (ldxq > kMax31 || ldwq > kMax31 || ldo > kMax31 || ldwe > ((int64_t)1 << 48))
+  if (ldxq > kMax31 || ldwq > kMaxLdw || ldo > kMax31 || ldwe > ((int64_t)1 << 48))
     return KQ_ERR_UNSUPPORTED;
   if (E > 1 && ldwe < (N - 1) * ldwq + rb) return KQ_ERR_INVALID_ARG;
   const size_t ss = scale_dtype == KQ_FP16 ? 2 : 4, os = out_dtype == KQ_FP32 ? 4 : 2;

@@ -30,7 +30,7 @@ template <>
 struct Elem<1> {
   typedef uint16_t raw;
   static __device__ __forceinline__ float get(raw v) { return (float)__builtin_bit_cast(_Float16, v); }
-  static __device__ __forceinline__ raw put(float v) { return __builtin_bit_cast(uint16_t, (_Float16)v); }
+  static __device__ __forceinline__ raw put(float v) { return __builtin_bit_cast(uint16_t, half_rne(v)); }
 };
 template <>
 struct Elem<2> {
