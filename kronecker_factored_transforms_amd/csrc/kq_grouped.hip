@@ -224,9 +224,9 @@ __global__ __launch_bounds__(WAVES * 64) void kq_grouped_stream_kernel(const Gro
 
 // ---- the tile kernel: 256 output channels x up to 256 rows of one group ----
 constexpr int kBM = 256, kBN = 256;
-constexpr int kStep = 128;                       // bytes of a row per step of the reduction
 constexpr int kTileWaves = 8;
-constexpr int kOpBytes = kBM * kStep;            // 32 KiB per operand and buffer
+constexpr int kStep = 128;             // bytes of every row per step of the reduction
+constexpr int kOpBytes = kBM * kStep;  // 32 KiB per operand and buffer, two buffers
 constexpr int kLoads = kOpBytes / 1024 / kTileWaves;
 static_assert(kBM == kBN && kLoads * 1024 * kTileWaves == kOpBytes, "one layout for both operands");
 
@@ -267,28 +267,30 @@ struct Share<8> {
 
 template <int BITS, int OUT, int NU>
 __device__ __forceinline__ void tile_product(const GroupedArgs &p, const RowTile &tile, int64_t n0,
-                                             unsigned char (*s_w)[kOpBytes], unsigned char (*s_x)[kOpBytes]) {
+                                             unsigned char *s_buf) {
   typedef Share<BITS> S;
   typedef typename S::acc_t acc_t;
   constexpr int kRegs = sizeof(acc_t) / 4;
+  constexpr int kChunks = kStep / 16, kRowsPer = 1024 / kStep;
   static_assert(S::kWN * S::kSide == 64 && S::kWM * S::kWN == kTileWaves, "blocks of a wave: 64 rows apart");
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int g = lane / S::kSide, lr = lane % S::kSide;
   const int wm = wave % S::kWM, wn = wave / S::kWM;
+  auto buf = [&](int b) { return s_buf + b * 2 * kOpBytes; };  // weight rows, then the tile's rows
 
-  // DMA: instruction J = wave kLoads + j of an operand fills tile rows 8 J .. 8 J + 7; lane i
-  // lands at row R = 8 J + i / 8, position i % 8, and reads piece (i % 8) ^ ((R / 2) % 8) of
-  // that row, so that the rows of one fragment read spread over all banks. Rows past the end
-  // of the weight or of the group read a valid row; their products are dropped.
+  // DMA: instruction J = wave kLoads + j of an operand fills kRowsPer tile rows; a lane lands
+  // at position lane % kChunks of row R and reads piece (lane % kChunks) ^ swz(R) of that row,
+  // so that the rows of one fragment read spread over all banks. Rows past the end of the
+  // weight or of the group read a valid row; their products are dropped.
+  auto swz = [](int R) { return (R >> 1) & 7; };
   const uint8_t *ax[kLoads];
   const uint8_t *wbase = uniform(p.wq + tile.e * p.ldwe + n0 * p.ldwq);
   uint32_t vw[kLoads];  // 256 rows of at most 16 MiB (checked on the host): 32 bits
-  const int piece0 = lane % 8;
 #pragma unroll
   for (int j = 0; j < kLoads; ++j) {
-    const int R = (wave * kLoads + j) * 8 + lane / 8;
-    const int piece = piece0 ^ ((R >> 1) & 7);
+    const int R = (wave * kLoads + j) * kRowsPer + lane / kChunks;
+    const int piece = (lane % kChunks) ^ swz(R);
     const int64_t n = n0 + R < p.N ? R : p.N - 1 - n0;
     vw[j] = (uint32_t)(n * p.ldwq + piece * 16);
     int64_t t = tile.begin + (R < tile.count ? R : 0);
@@ -296,26 +298,24 @@ __device__ __forceinline__ void tile_product(const GroupedArgs &p, const RowTile
     if (t < 0 || t >= p.T) t = 0;
     ax[j] = p.xq + t * p.ldxq + piece * 16;
   }
-  const int steps = (p.pieces + 7) / 8;
-  auto dma_step = [&](int ks, int b) {
-    if (ks * 8 + 8 <= p.pieces) {
+  const int steps = (p.pieces + kChunks - 1) / kChunks;
+  auto dma_step = [&](int ks, int b, int j0 = 0, int j1 = kLoads) {
+    if ((ks + 1) * kChunks <= p.pieces) {
       const uint8_t *w = wbase + (int64_t)ks * kStep;
 #pragma unroll
-      for (int j = 0; j < kLoads; ++j) {
-        dma16<false>(w, vw[j], lds_addr(s_w[b] + (wave * kLoads + j) * 1024));
-        if ((wave * kLoads + j) * 8 < 64 * NU)
-          dma16_addr<false>(ax[j], lds_addr(s_x[b] + (wave * kLoads + j) * 1024));
+      for (int j = j0; j < j1; ++j) {
+        dma16<false>(w, vw[j], lds_addr(buf(b) + (wave * kLoads + j) * 1024));
+        dma16_addr<false>(ax[j], lds_addr(buf(b) + kOpBytes + (wave * kLoads + j) * 1024));
         ax[j] += kStep;
       }
     } else {  // the last step of a row that ends inside it: the rest comes from a block of zeros
 #pragma unroll
-      for (int j = 0; j < kLoads; ++j) {
-        const int R = (wave * kLoads + j) * 8 + lane / 8;
-        const bool in = ks * 8 + (piece0 ^ ((R >> 1) & 7)) < p.pieces;
+      for (int j = j0; j < j1; ++j) {
+        const int R = (wave * kLoads + j) * kRowsPer + lane / kChunks;
+        const bool in = ks * kChunks + ((lane % kChunks) ^ swz(R)) < p.pieces;
         dma16_addr<false>(in ? wbase + (int64_t)ks * kStep + vw[j] : kZeros,
-                          lds_addr(s_w[b] + (wave * kLoads + j) * 1024));
-        if ((wave * kLoads + j) * 8 < 64 * NU)
-          dma16_addr<false>(in ? ax[j] : kZeros, lds_addr(s_x[b] + (wave * kLoads + j) * 1024));
+                          lds_addr(buf(b) + (wave * kLoads + j) * 1024));
+        dma16_addr<false>(in ? ax[j] : kZeros, lds_addr(buf(b) + kOpBytes + (wave * kLoads + j) * 1024));
       }
     }
   };
@@ -328,69 +328,120 @@ __device__ __forceinline__ void tile_product(const GroupedArgs &p, const RowTile
 #pragma unroll
       for (int r = 0; r < kRegs; ++r) acc[m][i][r] = 0;
 
-  // rows of this lane's fragments: (R / 2) % 8 is (lr / 2) % 8 for all of them
-  const int sw8 = (lr >> 1) & 7;
+  // rows of this lane's fragments: swz is swz(lr) for all of them
+  const int sl = swz(lr);
   const int row_w = wm * (kBM / S::kWM) + lr, row_x = wn * S::kSide + lr;
-  dma_step(0, 0);
-  for (int ks = 0; ks < steps; ++ks) {
-    const int b = ks & 1;
-    // this step's tiles have landed, for every wave; every wave is also done reading the
-    // other buffer, which the next DMA overwrites
-    wait_and_fence<kWaitVm0>();
-    __builtin_amdgcn_s_barrier();
-    __builtin_amdgcn_sched_barrier(0);
-    asm volatile("" ::: "memory");
-    if (ks + 1 < steps) dma_step(ks + 1, b ^ 1);
+  // The steps of this lane's rows, and which of them are written: loaded here, so that the
+  // epilogue does not wait for them (a row's number, then its step) row by row.
+  float sx[NU];
+  int written = 0;
+#pragma unroll
+  for (int i = 0; i < NU; ++i) {
+    const int R = row_x + i * 64;
+    int64_t t = tile.begin + (R < tile.count ? R : 0);
+    if (p.rows) t = p.rows[t];
+    const bool in = t >= 0 && t < p.T;
+    sx[i] = load_step(p.sx, in ? t : 0, p.scale_fp16);
+    if (R < tile.count && in) written |= 1 << i;
+  }
+
+  // A step's fragments come in kParts parts, each read while the part before it multiplies;
+  // the first part of the next step is read before the last one of this step multiplies.
+  constexpr int kParts = kStep / (1024 / S::kSide);
+  struct Part {
+    u32x4_t w[S::kMI], x[NU];
+  };
+  auto read_part = [&](const unsigned char *w, int q) {
+    Part f;
+    const int off = ((64 / S::kSide * q + g) ^ sl) * 16;
+#pragma unroll
+    for (int m = 0; m < S::kMI; ++m)
+      f.w[m] = *reinterpret_cast<const u32x4_t *>(w + (row_w + m * S::kSide) * kStep + off);
+#pragma unroll
+    for (int i = 0; i < NU; ++i)
+      f.x[i] = *reinterpret_cast<const u32x4_t *>(w + kOpBytes + (row_x + i * 64) * kStep + off);
+    return f;
+  };
+  auto multiply = [&](const Part &f) {
     if constexpr (BITS == 4) {
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {  // 64 bytes (128 codes): two instructions' depth
-        const int off = ((4 * q + g) ^ sw8) * 16;
-        u32x4_t pa[S::kMI], pb[NU];
+      for (int h = 0; h < 2; ++h) {
+        i32x4 a[S::kMI], bx[NU];
 #pragma unroll
         for (int m = 0; m < S::kMI; ++m)
-          pa[m] = *reinterpret_cast<const u32x4_t *>(s_w[b] + (row_w + m * 16) * kStep + off);
+          a[m] = h ? unpack16(f.w[m].z, f.w[m].w) : unpack16(f.w[m].x, f.w[m].y);
 #pragma unroll
         for (int i = 0; i < NU; ++i)
-          pb[i] = *reinterpret_cast<const u32x4_t *>(s_x[b] + (row_x + i * 64) * kStep + off);
+          bx[i] = h ? unpack16(f.x[i].z, f.x[i].w) : unpack16(f.x[i].x, f.x[i].y);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          i32x4 a[S::kMI], bx[NU];
-#pragma unroll
-          for (int m = 0; m < S::kMI; ++m)
-            a[m] = h ? unpack16(pa[m].z, pa[m].w) : unpack16(pa[m].x, pa[m].y);
+        for (int m = 0; m < S::kMI; ++m)
 #pragma unroll
           for (int i = 0; i < NU; ++i)
-            bx[i] = h ? unpack16(pb[i].z, pb[i].w) : unpack16(pb[i].x, pb[i].y);
-#pragma unroll
-          for (int m = 0; m < S::kMI; ++m)
-#pragma unroll
-            for (int i = 0; i < NU; ++i)
-              acc[m][i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a[m], bx[i], acc[m][i], 0, 0, 0);
-        }
+            acc[m][i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a[m], bx[i], acc[m][i], 0, 0, 0);
       }
     } else {
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {  // 32 bytes (32 codes)
-        const int off = ((2 * q + g) ^ sw8) * 16;
-        i32x4 pa[S::kMI], pb[NU];
-#pragma unroll
-        for (int m = 0; m < S::kMI; ++m)
-          pa[m] = *reinterpret_cast<const i32x4 *>(s_w[b] + (row_w + m * 32) * kStep + off);
+      for (int m = 0; m < S::kMI; ++m)
 #pragma unroll
         for (int i = 0; i < NU; ++i)
-          pb[i] = *reinterpret_cast<const i32x4 *>(s_x[b] + (row_x + i * 64) * kStep + off);
+          acc[m][i] = __builtin_amdgcn_mfma_i32_32x32x32_i8(
+              __builtin_bit_cast(i32x4, f.w[m]), __builtin_bit_cast(i32x4, f.x[i]), acc[m][i], 0, 0, 0);
+    }
+  };
+  auto sync = [] {
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("" ::: "memory");
+  };
+  dma_step(0, 0);
+  if constexpr (BITS == 4) {
+    // two waves of a SIMD cover each other's reads; a second part in registers would not fit
+    for (int ks = 0; ks < steps; ++ks) {
+      wait_and_fence<kWaitVm0>();
+      sync();  // this step has landed for every wave, and every wave is done with the one before
+      if (ks + 1 < steps) dma_step(ks + 1, (ks + 1) & 1);
 #pragma unroll
-        for (int m = 0; m < S::kMI; ++m)
+      for (int q = 0; q < kParts; ++q) multiply(read_part(buf(ks & 1), q));
+      wait_and_fence<kWaitLgkm0>();
+    }
+  } else {
+    // each part is read while the one before it multiplies, across the steps
+    if (steps > 1) {
+      dma_step(1, 1);
+      wait_and_fence<wait_vm_imm(2 * kLoads)>();
+    } else {
+      wait_and_fence<kWaitVm0>();
+    }
+    sync();
+    Part f = read_part(buf(0), 0);
+    for (int ks = 0; ks < steps; ++ks) {
+      const int b = ks & 1;
 #pragma unroll
-          for (int i = 0; i < NU; ++i)
-            acc[m][i] = __builtin_amdgcn_mfma_i32_32x32x32_i8(pa[m], pb[i], acc[m][i], 0, 0, 0);
+      for (int q = 0; q < kParts; ++q) {
+        Part next = f;
+        if (q + 1 < kParts) {
+          next = read_part(buf(b), q + 1);
+        } else if (ks + 1 < steps) {
+          // this wave's reads of buffer b have returned, and its loads of the next step have
+          // landed; behind the barrier that holds for every wave, so b may be overwritten and
+          // the other buffer read
+          wait_and_fence<kWaitLgkm0>();
+          wait_and_fence<kWaitVm0>();
+          sync();
+          next = read_part(buf(b ^ 1), 0);
+          if (ks + 2 < steps) dma_step(ks + 2, b);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        multiply(f);
+        __builtin_amdgcn_sched_barrier(0);
+        f = next;
       }
     }
-    wait_and_fence<kWaitLgkm0>();  // this wave's reads of buffer b have returned
   }
 
-  // lane: row i * 64 + wn * side + lr; per group of 4 registers 4 consecutive channels. The
-  // channels' steps first, then row by row.
+  // Epilogue: a lane holds row wn * side + lr of each block and, per group of 4 registers, 4
+  // consecutive channels. (Staging the rows in LDS for whole-line stores was slower: 1055 us
+  // against 1018 on 16384 x 14336 x 4096 INT8, its barriers cost more than the stores gained.)
   constexpr int kQ = S::kMI * kRegs / 4;  // groups of 4 channels
   const int64_t nl = n0 + wm * (kBM / S::kWM) + 4 * g;  // group q: nl + group_at(q)
   auto group_at = [](int q) { return q / (kRegs / 4) * S::kSide + q % (kRegs / 4) * 4 * (64 / S::kSide); };
@@ -398,19 +449,15 @@ __device__ __forceinline__ void tile_product(const GroupedArgs &p, const RowTile
   load_steps<kQ>(p.sw, tile.e * p.N, nl, p.N, p.scale_fp16, group_at, sw);
 #pragma unroll
   for (int i = 0; i < NU; ++i) {
-    const int R = row_x + i * 64;
-    if (R >= tile.count) continue;
-    const int64_t t = p.rows ? (int64_t)p.rows[tile.begin + R] : tile.begin + R;
-    if (t < 0 || t >= p.T) continue;
-    const float sx = load_step(p.sx, t, p.scale_fp16);
-    const int64_t row = (tile.begin + R) * p.ldo + nl;
+    if (!(written >> i & 1)) continue;
+    const int64_t row = (tile.begin + row_x + i * 64) * p.ldo + nl;
 #pragma unroll
     for (int q = 0; q < kQ; ++q) {
       float v[4];
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const int a = acc[q / (kRegs / 4)][i][q % (kRegs / 4) * 4 + r];
-        v[r] = __fmul_rn(__fmul_rn((float)(BITS == 8 ? a : a >> 8), sx), sw[q][r]);
+        v[r] = __fmul_rn(__fmul_rn((float)(BITS == 8 ? a : a >> 8), sx[i]), sw[q][r]);
       }
       store_out4<OUT>(p.out, row + group_at(q), v, p.N - nl - group_at(q));
     }
@@ -419,15 +466,14 @@ __device__ __forceinline__ void tile_product(const GroupedArgs &p, const RowTile
 
 template <int BITS, int OUT>
 __global__ __launch_bounds__(kTileWaves * 64) void kq_grouped_tile_kernel(const GroupedArgs p, int tiles_m) {
-  __shared__ __align__(16) unsigned char s_w[2][kOpBytes];
-  __shared__ __align__(16) unsigned char s_x[2][kOpBytes];
+  __shared__ __align__(16) unsigned char s_buf[4 * kOpBytes];
   const RowTile tile = find_tile<kBN>(p.offsets, p.E, p.R, (int)(blockIdx.x / tiles_m));
   if (tile.e < 0) return;
   const int64_t n0 = (int64_t)(blockIdx.x % tiles_m) * kBM;
-  if (tile.count > 192) tile_product<BITS, OUT, 4>(p, tile, n0, s_w, s_x);
-  else if (tile.count > 128) tile_product<BITS, OUT, 3>(p, tile, n0, s_w, s_x);
-  else if (tile.count > 64) tile_product<BITS, OUT, 2>(p, tile, n0, s_w, s_x);
-  else tile_product<BITS, OUT, 1>(p, tile, n0, s_w, s_x);
+  if (tile.count > 192) tile_product<BITS, OUT, 4>(p, tile, n0, s_buf);
+  else if (tile.count > 128) tile_product<BITS, OUT, 3>(p, tile, n0, s_buf);
+  else if (tile.count > 64) tile_product<BITS, OUT, 2>(p, tile, n0, s_buf);
+  else tile_product<BITS, OUT, 1>(p, tile, n0, s_buf);
 }
 
 template <int BITS>
