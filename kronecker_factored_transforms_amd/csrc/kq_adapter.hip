@@ -14,6 +14,7 @@
 // batch's blocks are loaded several at a time.
 #include "kq_internal.h"
 #include "kq_common.h"
+#include "kq_device.h"
 
 namespace {
 
@@ -47,11 +48,19 @@ struct AdapterArgs {
   const int32_t *adapter;
   const float *scaling;
   void *out;
-  float *part;  // [splits][T][r16] parts of h
+  void *ws;  // h: parts or operands (see Workspace)
   int64_t ldx, ldb, ldo, T;
-  int K, N, r, r16, L, splits, split_steps;  // a step: 32 values of K
-  int tiles_per_group;                       // up: token tiles of one workgroup
+  int K, N, r, L, splits, split_steps;  // a step: kStep values of K
+  int tiles_per_group;                  // up: token tiles of one workgroup
 };
+
+// What lies between the two kernels. Few tokens: the parts of h over K, fp32,
+// [splits][T][ranks up to a multiple of 16]. Many (one part): h as the second product's
+// operands, [tile of 16 tokens][steps of 32 ranks][first, second term][lane][8 values], and the
+// exponent of the power of two each token's h was multiplied by, [tile][16].
+constexpr int64_t kWide = 4096;  // from this many tokens on: operands
+
+__device__ __forceinline__ int round16(int r) { return (r + 15) / 16 * 16; }
 
 // Token t's adapter, -1 for none
 __device__ __forceinline__ int token_adapter(const AdapterArgs &p, int64_t t) {
@@ -68,184 +77,365 @@ __device__ __forceinline__ int next_adapter(unsigned long long &left, int l) {
   return a;
 }
 
-// h's parts. A workgroup takes TF blocks of 16 tokens and a share of K, which its waves split
-// again and add up in LDS. D adapters at a time (their matrices' loads overlap), RB blocks of 16
-// ranks, U steps of K in flight.
-template <int DT, int RB, int TF, int WAVES, int D, int U>
-__global__ __launch_bounds__(WAVES * 64) void kq_adapter_down_kernel(const AdapterArgs p) {
+// h of one token (lane: ranks 32 s + 8 g + 0..7) as two 16-bit terms. fp16: a power of two per
+// token brings its h into the type's range (exact; undone on the sums), so that neither term
+// overflows or loses bits; returns its exponent. bf16 has fp32's range.
+template <int DT, int RS>
+__device__ __forceinline__ int two_terms(const float (&h)[RS][8], typename Half<DT>::vec (&hi)[RS],
+                                         typename Half<DT>::vec (&lo)[RS]) {
+  typedef typename Half<DT>::one one;
+  int ex = 0;
+  if constexpr (DT == 1) {
+    float top = 0.f;
+#pragma unroll
+    for (int s = 0; s < RS; ++s)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(h[s][e]));
+    top = fmaxf(top, __shfl_xor(top, 16, 64));
+    top = fmaxf(top, __shfl_xor(top, 32, 64));
+    const int be = (int)(__float_as_uint(top) >> 23);
+    ex = be == 0 || be == 255 ? 0 : 127 + 14 - be;
+  }
+#pragma unroll
+  for (int s = 0; s < RS; ++s)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float v = DT == 1 ? __builtin_ldexpf(h[s][e], ex) : h[s][e];
+      const one a = Half<DT>::round(v);
+      hi[s][e] = a;
+      lo[s][e] = Half<DT>::round(__builtin_isfinite((float)a) ? __fsub_rn(v, (float)a) : 0.f);
+    }
+  return ex;
+}
+
+constexpr int kStep = 64;  // values of K per step: rows of 128 bytes in LDS
+__device__ __align__(16) const unsigned char kZeroPiece[16] = {};
+
+__device__ __forceinline__ const unsigned char *uniform(const void *p) {
+  const uint64_t v = reinterpret_cast<uint64_t>(p);
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v);
+  const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
+  return reinterpret_cast<const unsigned char *>((uint64_t)hi << 32 | lo);
+}
+
+// The products of DD adapters' A (numbers a[]) with TF blocks of 16 tokens, over one wave's steps
+// s0, s0 + WAVES, .. of K below s1; RB blocks of 16 ranks. Rows come by DMA into the wave's own
+// ring of LDS (no barrier), 8 rows of 128 bytes at a time: read straight into the operands, 16
+// rows lie behind each other's 16 bytes and every lane is a memory access of its own. Piece p of
+// row R lies at position p ^ ((R / 2) % 8): the 16 rows of a fragment read spread over all banks.
+template <int DT, int RB, int TF, int WAVES, int DD, int RING>
+__device__ __forceinline__ void down_product(const AdapterArgs &p, int64_t t0, const int *a, int s0, int s1,
+                                             unsigned char *ring, f32x4 (&acc)[DD][RB][TF]) {
   typedef typename Half<DT>::vec vec;
-  __shared__ f32x4 s_acc[WAVES][D * RB * TF][64];
+  constexpr int kX = 2 * TF, kA = 2 * RB;           // DMA instructions for x, for one A
+  constexpr int kLoads = kX + DD * kA;              // per step
+  constexpr int kMost = RING / (kLoads * 1024);
+  constexpr int kStages = kMost > 4 ? 4 : kMost;
+  static_assert(kStages >= 2 && kLoads * (kStages - 1) < 64, "two steps in LDS, loads within the counter");
+  const int lane = threadIdx.x & 63, g = lane >> 4, lr = lane & 15;
+  // offsets from x's row t0 and from A's first row; rows past the end read a valid row, and
+  // what comes of them is dropped
+  uint32_t vx[kX], va[kA];
+  int piece[2];  // of an even and an odd instruction's rows
+#pragma unroll
+  for (int j = 0; j < 2; ++j) piece[j] = (lane % 8) ^ (((8 * j + lane / 8) >> 1) & 7);
+#pragma unroll
+  for (int j = 0; j < kX; ++j) {
+    const int R = 8 * j + lane / 8;
+    const int64_t row = t0 + R < p.T ? R : p.T - 1 - t0;
+    vx[j] = (uint32_t)(row * p.ldx * 2 + piece[j % 2] * 16);
+  }
+#pragma unroll
+  for (int j = 0; j < kA; ++j) va[j] = (uint32_t)min(8 * j + lane / 8, p.r - 1) * (uint32_t)(p.K * 2) + piece[j % 2] * 16;
+  const unsigned char *x = uniform(reinterpret_cast<const uint16_t *>(p.x) + t0 * p.ldx);
+  const unsigned char *am[DD];
+#pragma unroll
+  for (int d = 0; d < DD; ++d)
+    am[d] = uniform(reinterpret_cast<const uint16_t *>(p.A) + (int64_t)a[d] * p.r * p.K);
+#pragma unroll
+  for (int d = 0; d < DD; ++d)
+#pragma unroll
+    for (int b = 0; b < RB; ++b)
+#pragma unroll
+      for (int f = 0; f < TF; ++f) acc[d][b][f] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const int pieces = p.K / 8;
+  auto load_step = [&](int s, int b) {
+    unsigned char *to = ring + b * (kLoads * 1024);
+    const int64_t o = (int64_t)s * (kStep * 2);
+    if (s * 8 + 8 <= pieces) {
+#pragma unroll
+      for (int j = 0; j < kX; ++j) dma16<false>(x + o, vx[j], lds_addr(to + j * 1024));
+#pragma unroll
+      for (int d = 0; d < DD; ++d)
+#pragma unroll
+        for (int j = 0; j < kA; ++j) dma16<false>(am[d] + o, va[j], lds_addr(to + (kX + d * kA + j) * 1024));
+    } else {  // the rows end inside this step: the rest comes from a block of zeros
+#pragma unroll
+      for (int j = 0; j < kX; ++j)
+        dma16_addr<false>(s * 8 + piece[j % 2] < pieces ? x + o + vx[j] : kZeroPiece, lds_addr(to + j * 1024));
+#pragma unroll
+      for (int d = 0; d < DD; ++d)
+#pragma unroll
+        for (int j = 0; j < kA; ++j)
+          dma16_addr<false>(s * 8 + piece[j % 2] < pieces ? am[d] + o + va[j] : kZeroPiece,
+                            lds_addr(to + (kX + d * kA + j) * 1024));
+    }
+  };
+  const int steps = s0 < s1 ? (s1 - s0 + WAVES - 1) / WAVES : 0;
+#pragma unroll
+  for (int k = 0; k < kStages - 1; ++k)
+    if (k < steps) load_step(s0 + k * WAVES, k);
+  const int sw = (lr >> 1) & 7;
+  int b = 0;
+  for (int k = 0; k < steps; ++k) {
+    if (k + kStages - 1 < steps) {
+      load_step(s0 + (k + kStages - 1) * WAVES, b == 0 ? kStages - 1 : b - 1);
+      wait_and_fence<wait_vm_imm(kLoads * (kStages - 1))>();
+    } else {
+      wait_and_fence<kWaitVm0>();
+    }
+    const unsigned char *from = ring + b * (kLoads * 1024);
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const int off = lr * 128 + ((4 * q + g) ^ sw) * 16;
+      vec xv[TF];
+#pragma unroll
+      for (int f = 0; f < TF; ++f) xv[f] = *reinterpret_cast<const vec *>(from + f * 2048 + off);
+#pragma unroll
+      for (int d = 0; d < DD; ++d)
+#pragma unroll
+        for (int rb = 0; rb < RB; ++rb) {
+          const vec av = *reinterpret_cast<const vec *>(from + (kX + d * kA + 2 * rb) * 1024 + off);
+#pragma unroll
+          for (int f = 0; f < TF; ++f) acc[d][rb][f] = Half<DT>::mma(av, xv[f], acc[d][rb][f]);
+        }
+    }
+    wait_and_fence<kWaitLgkm0>();  // this step's reads have returned: its place may be overwritten
+    b = b + 1 == kStages ? 0 : b + 1;
+  }
+}
+
+// h of TF blocks of 16 tokens over a share of K, which the waves split again and add up in LDS;
+// D adapters at a time. OPERANDS: h is whole, and is left scaled and as operands.
+template <int DT, int RB, int TF, int WAVES, int D, int RING, bool OPERANDS>
+__global__ __launch_bounds__(WAVES * 64) void kq_adapter_down_kernel(const AdapterArgs p) {
+  constexpr int RS = (RB + 1) / 2;
+  constexpr int kRow = 32 * RS + 4;  // of h in LDS, floats: rows 4 banks apart
+  constexpr int kSum = WAVES * D * RB * TF * 1024, kH = OPERANDS ? 16 * TF * kRow * 4 : 0;
+  constexpr int kAcc = kSum + kH;
+  constexpr int kLds = WAVES * RING > kAcc ? WAVES * RING : kAcc;
+  __shared__ __align__(16) unsigned char s_mem[kLds];
+  f32x4 *s_acc = reinterpret_cast<f32x4 *>(s_mem);           // [WAVES][D RB TF][64], behind the rings' use
+  float *s_h = reinterpret_cast<float *>(s_mem + kLds - kH);  // [16 TF][kRow]
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int g = lane >> 4, lr = lane & 15;
   const int64_t t0 = (int64_t)blockIdx.x * (16 * TF);
-  int l[TF];
-  const uint16_t *xrow[TF];
   // lanes 0..15 of the wave stand for block 0's tokens, 16..31 for block 1's
   const int mine = token_adapter(p, t0 + (lane & (16 * TF - 1)));
+  int l[TF];
 #pragma unroll
-  for (int f = 0; f < TF; ++f) {
-    l[f] = __shfl(mine, 16 * f + lr, 64);
-    const int64_t t = t0 + 16 * f + lr;
-    xrow[f] = reinterpret_cast<const uint16_t *>(p.x) + (t < p.T ? t : p.T - 1) * p.ldx;
-  }
-  const int s0 = blockIdx.y * p.split_steps;
-  const int s1 = min((p.K + 31) / 32, s0 + p.split_steps);
+  for (int f = 0; f < TF; ++f) l[f] = __shfl(mine, 16 * f + lr, 64);
+  const int s0 = blockIdx.y * p.split_steps + wave;
+  const int s1 = min((p.K + kStep - 1) / kStep, ((int)blockIdx.y + 1) * p.split_steps);
+  f32x4 kept[OPERANDS ? (RB * TF + WAVES - 1) / WAVES : 1];  // this wave's blocks of h, of all adapters
+#pragma unroll
+  for (f32x4 &v : kept) v = f32x4{0.f, 0.f, 0.f, 0.f};
   unsigned long long left = __ballot(mine >= 0) & ((1ull << (16 * TF)) - 1);
+  auto put = [&](int d, const f32x4 (&acc)[RB][TF]) {  // one adapter's accumulators of this wave
+#pragma unroll
+    for (int b = 0; b < RB; ++b)
+#pragma unroll
+      for (int f = 0; f < TF; ++f) s_acc[((wave * D + d) * RB * TF + b * TF + f) * 64 + lane] = acc[b][f];
+  };
+  auto sum = [&](int a, int d) {  // lane: ranks 16 b + 4 g + 0..3 of token 16 f + lr
+#pragma unroll
+    for (int b = 0; b < RB; ++b)
+#pragma unroll
+      for (int f = 0; f < TF; ++f) {
+        const int i = b * TF + f;
+        if (i % WAVES != wave) continue;
+        f32x4 v = s_acc[(d * RB * TF + i) * 64 + lane];
+#pragma unroll
+        for (int w = 1; w < WAVES; ++w) v += s_acc[((w * D + d) * RB * TF + i) * 64 + lane];
+        if (l[f] != a) continue;
+        if constexpr (OPERANDS)
+          kept[i / WAVES] = v;
+        else if (16 * b < round16(p.r))
+          *reinterpret_cast<f32x4 *>(reinterpret_cast<float *>(p.ws) +
+                                     ((int64_t)blockIdx.y * p.T + t0 + 16 * f + lr) * round16(p.r) + 16 * b +
+                                     4 * g) = v;
+      }
+  };
   while (left) {
-    int a[D];
-    const uint16_t *am[D];
+    int a[D], n = 0;
 #pragma unroll
     for (int d = 0; d < D; ++d) {
-      a[d] = next_adapter(left, mine);
-      am[d] = reinterpret_cast<const uint16_t *>(p.A) + (int64_t)max(a[d], 0) * p.r * p.K;
+      const int next = next_adapter(left, mine);
+      a[d] = next < 0 ? a[0] : next;  // a short group's rest: its first adapter again, dropped
+      n += next >= 0;
     }
-    f32x4 acc[D][RB][TF];
+    unsigned char *ring = s_mem + wave * RING;
+    if (n == 1) {
+      f32x4 acc[1][RB][TF];
+      down_product<DT, RB, TF, WAVES, 1, RING>(p, t0, a, s0, s1, ring, acc);
+      lds_barrier();
+      put(0, acc[0]);
+    } else if constexpr (D > 1) {
+      f32x4 acc[D][RB][TF];
+      down_product<DT, RB, TF, WAVES, D, RING>(p, t0, a, s0, s1, ring, acc);
+      lds_barrier();
 #pragma unroll
-    for (int d = 0; d < D; ++d)
-#pragma unroll
-      for (int b = 0; b < RB; ++b)
-#pragma unroll
-        for (int f = 0; f < TF; ++f) acc[d][b][f] = f32x4{0.f, 0.f, 0.f, 0.f};
-    for (int s = s0 + wave; s < s1; s += WAVES * U) {
-      u32x4_t xv[U][TF], av[U][D][RB];
-      const u32x4_t zero = {0, 0, 0, 0};
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int k = (s + u * WAVES) * 32 + g * 8;
-        const bool in = s + u * WAVES < s1 && k < p.K;  // behind the end: zeros on both sides
-#pragma unroll
-        for (int f = 0; f < TF; ++f)
-          xv[u][f] = in ? *reinterpret_cast<const u32x4_t *>(xrow[f] + k) : zero;
-#pragma unroll
-        for (int d = 0; d < D; ++d)
-#pragma unroll
-          for (int b = 0; b < RB; ++b) {
-            const int row = min(16 * b + lr, p.r - 1);  // ranks past r: dropped below
-            av[u][d][b] = in && a[d] >= 0
-                              ? *reinterpret_cast<const u32x4_t *>(am[d] + (int64_t)row * p.K + k)
-                              : zero;
-          }
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int d = 0; d < D; ++d)
-#pragma unroll
-          for (int b = 0; b < RB; ++b)
-#pragma unroll
-            for (int f = 0; f < TF; ++f)
-              acc[d][b][f] = Half<DT>::mma(__builtin_bit_cast(vec, av[u][d][b]),
-                                           __builtin_bit_cast(vec, xv[u][f]), acc[d][b][f]);
+      for (int d = 0; d < D; ++d) put(d, acc[d]);
     }
-#pragma unroll
-    for (int d = 0; d < D; ++d)
-#pragma unroll
-      for (int b = 0; b < RB; ++b)
-#pragma unroll
-        for (int f = 0; f < TF; ++f) s_acc[wave][(d * RB + b) * TF + f][lane] = acc[d][b][f];
     lds_barrier();
-    // lane: ranks 16 b + 4 g + 0..3 of token 16 f + lr
 #pragma unroll
     for (int d = 0; d < D; ++d)
+      if (d < n) sum(a[d], d);
+    lds_barrier();  // before the rings are written again
+  }
+  if constexpr (OPERANDS) {
 #pragma unroll
-      for (int b = 0; b < RB; ++b)
+    for (int b = 0; b < RB; ++b)
 #pragma unroll
-        for (int f = 0; f < TF; ++f) {
-          const int i = (d * RB + b) * TF + f;
-          if (i % WAVES != wave) continue;
-          f32x4 v = s_acc[0][i][lane];
+      for (int f = 0; f < TF; ++f) {
+        const int i = b * TF + f;
+        if (i % WAVES == wave)
+          *reinterpret_cast<f32x4 *>(s_h + (16 * f + lr) * kRow + 16 * b + 4 * g) = kept[i / WAVES];
+      }
+    lds_barrier();
+    for (int f = wave; f < TF; f += WAVES) {
+      const int lf = __shfl(mine, 16 * f + lr, 64);
+      const float sc = lf >= 0 && p.scaling ? p.scaling[lf] : 1.0f;
+      float h[RS][8];
 #pragma unroll
-          for (int w = 1; w < WAVES; ++w) v += s_acc[w][i][lane];
-          if (a[d] >= 0 && l[f] == a[d] && 16 * b < p.r16)
-            *reinterpret_cast<f32x4 *>(p.part + ((int64_t)blockIdx.y * p.T + t0 + 16 * f + lr) * p.r16 +
-                                       16 * b + 4 * g) = v;
+      for (int s = 0; s < RS; ++s)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int k = 32 * s + 8 * g + e;
+          h[s][e] = k < p.r ? __fmul_rn(s_h[(16 * f + lr) * kRow + k], sc) : 0.f;
         }
-    if (left) lds_barrier();  // before s_acc is written again
+      typename Half<DT>::vec hi[RS], lo[RS];
+      const int ex = two_terms<DT, RS>(h, hi, lo);
+      const int64_t tile = t0 / 16 + f, tiles = (p.T + 15) / 16;
+      if (tile < tiles) {
+        auto *o = reinterpret_cast<typename Half<DT>::vec *>(p.ws) + tile * (RS * 2 * 64) + lane;
+#pragma unroll
+        for (int s = 0; s < RS; ++s) {
+          o[(2 * s) * 64] = hi[s];
+          o[(2 * s + 1) * 64] = lo[s];
+        }
+        if (lane < 16)
+          (reinterpret_cast<int *>(reinterpret_cast<typename Half<DT>::vec *>(p.ws) + tiles * (RS * 2 * 64)))[tile * 16 + lane] = ex;
+      }
+    }
   }
 }
 
 constexpr int kUpWaves = 4;
 
-// out. A workgroup takes 64 NB columns (16 NB per wave) of tiles_per_group tiles of 16 tokens; RS
-// steps of 32 ranks; D adapters' B at a time. The rows of a B block are dealt so that a lane
-// ends with 4 NB consecutive columns of one token.
-template <int DT, int RS, int NB, int D>
+// out. A workgroup takes 256 columns (64 per wave; 32 beyond 64 ranks) of tiles_per_group tiles
+// of 16 tokens; RS steps of 32 ranks; D adapters' B at a time. A tile's sums go through the
+// wave's own part of LDS, so that 8 (4) lanes read and write the 128 (64) bytes of one row of
+// base and out: in the product's own layout every lane is a row of its own, and each 16 bytes a
+// memory access of its own. A tile's base and h are on their way while the one before it is
+// computed. OPERANDS: what lies between the kernels, see above.
+template <int RS>
+constexpr int kUpBlocks = RS <= 2 ? 4 : 2;  // blocks of 16 columns per wave: their B in registers
+
+template <int DT, int RS, int D, bool OPERANDS>
 __global__ __launch_bounds__(kUpWaves * 64) void kq_adapter_up_kernel(const AdapterArgs p) {
   typedef typename Half<DT>::vec vec;
   typedef typename Half<DT>::one one;
-  constexpr int kW = 4 * NB / 8;  // 16-byte words of a lane's columns
+  constexpr int NB = kUpBlocks<RS>, kRow = 16 * NB + 4;  // floats of a row in LDS: all banks in turn
+  constexpr int kLanes = 2 * NB, kPasses = NB / 2;       // lanes of a row of base and out
+  __shared__ __align__(16) float s_out[kUpWaves][16 * kRow];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int g = lane >> 4, lr = lane & 15;
   const int n0 = (int)(blockIdx.x * kUpWaves + wave) * 16 * NB;
   if (n0 >= p.N) return;  // whole waves; there is no barrier here
   int64_t tile = (int64_t)blockIdx.y * p.tiles_per_group;
-  const int64_t last = min(tile + p.tiles_per_group, (p.T + 15) / 16);
-  const uint32_t col = (uint32_t)(4 * NB * (lr >> 2) + (lr & 3));  // of block j: + 4 j
-  const int nl = n0 + 4 * NB * g;                                  // this lane's first column
-  u32x4_t bv[D][NB][RS];
-  int held = -1;  // the adapter in bv[0]
-  for (; tile < last; ++tile) {
-    const int64_t t = tile * 16 + lr;
-    const bool live = t < p.T;
-    // everything that does not wait for something else first: the adapter, base, h's parts
-    const int l = token_adapter(p, t);
-    u32x4_t bs[kW];
+  const int64_t tiles = (p.T + 15) / 16, last = min(tile + p.tiles_per_group, tiles);
+  uint32_t brow[NB];  // this lane's rows of B, in values; columns past N: dropped below
 #pragma unroll
-    for (int w = 0; w < kW; ++w) {
-      bs[w] = u32x4_t{0, 0, 0, 0};
-      if (p.base && live && nl + 8 * w < p.N)
-        bs[w] = *reinterpret_cast<const u32x4_t *>(reinterpret_cast<const one *>(p.base) + t * p.ldb + nl + 8 * w);
+  for (int j = 0; j < NB; ++j) brow[j] = (uint32_t)min(n0 + 16 * j + lr, p.N - 1) * (uint32_t)p.r;
+  uint32_t rank[RS];  // this lane's 8 ranks of step s; past r: the first ones, made 0
+#pragma unroll
+  for (int s = 0; s < RS; ++s) rank[s] = 32 * s + 8 * g < p.r ? 32 * s + 8 * g : 0;
+  const int tr = lane / kLanes, nc = n0 + 8 * (lane % kLanes);  // base and out: this lane's token and columns
+  const bool in = nc < p.N;  // N is a multiple of 8: a word is all in or all out
+  float *mine = s_out[wave];
+
+  struct Tile {
+    int l, ex;
+    u32x4_t base[kPasses];
+    vec hi[RS], lo[RS];
+  };
+  auto load_tile = [&](int64_t tile) {
+    Tile v;
+    const int64_t t = tile * 16 + lr, tc = t < p.T ? t : p.T - 1;
+    v.l = token_adapter(p, t);
+    v.ex = 0;
+#pragma unroll
+    for (int w = 0; w < kPasses; ++w) {
+      const int64_t tb = tile * 16 + tr + 64 / kLanes * w;
+      v.base[w] = u32x4_t{0, 0, 0, 0};
+      if (p.base && in && tb < p.T)
+        v.base[w] = *reinterpret_cast<const u32x4_t *>(reinterpret_cast<const one *>(p.base) + tb * p.ldb + nc);
     }
-    float h[RS][8];
-#pragma unroll
-    for (int s = 0; s < RS; ++s)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) h[s][e] = 0.f;
-    for (int i = 0; i < p.splits; ++i) {
+    if constexpr (OPERANDS) {
+      const vec *o = reinterpret_cast<const vec *>(p.ws) + tile * (RS * 2 * 64) + lane;
 #pragma unroll
       for (int s = 0; s < RS; ++s) {
-        const int k = 32 * s + 8 * g;
-        if (l >= 0 && k < p.r) {
-          const f32x4 *q = reinterpret_cast<const f32x4 *>(p.part + ((int64_t)i * p.T + t) * p.r16 + k);
-          const f32x4 a = q[0], b = q[1];
+        v.hi[s] = o[(2 * s) * 64];
+        v.lo[s] = o[(2 * s + 1) * 64];
+      }
+      if constexpr (DT == 1)
+        v.ex = (reinterpret_cast<const int *>(reinterpret_cast<const vec *>(p.ws) + tiles * (RS * 2 * 64)))[tile * 16 + lr];
+    } else {
+      // h of a token without an adapter is what the workspace holds, and dropped
+      const int r16 = round16(p.r);
+      const float *q = reinterpret_cast<const float *>(p.ws) + tc * r16;
+      constexpr int kAt = RS <= 4 ? 8 / RS : 1;  // parts on their way at a time
+      float h[RS][8];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            h[s][e] += a[e];
-            h[s][4 + e] += b[e];
-          }
+      for (int s = 0; s < RS; ++s)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) h[s][e] = 0.f;
+      for (int i = 0; i < p.splits; i += kAt) {
+        f32x4 w[kAt][RS][2];
+#pragma unroll
+        for (int k = 0; k < kAt; ++k) {
+          const float *qi = q + (int64_t)min(i + k, p.splits - 1) * p.T * r16;
+#pragma unroll
+          for (int s = 0; s < RS; ++s)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) w[k][s][e] = *reinterpret_cast<const f32x4 *>(qi + rank[s] + 4 * e);
         }
+#pragma unroll
+        for (int k = 0; k < kAt; ++k)
+          if (i + k < p.splits)
+#pragma unroll
+            for (int s = 0; s < RS; ++s)
+#pragma unroll
+              for (int e = 0; e < 8; ++e) h[s][e] += w[k][s][e / 4][e % 4];
       }
+      const float sc = v.l >= 0 && p.scaling ? p.scaling[v.l] : 1.0f;
+#pragma unroll
+      for (int s = 0; s < RS; ++s)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) h[s][e] = 32 * s + 8 * g < p.r ? __fmul_rn(h[s][e], sc) : 0.f;
+      v.ex = two_terms<DT, RS>(h, v.hi, v.lo);
     }
-    // h of token lr, ranks 32 s + 8 g + 0..7, as two 16-bit terms
-    const float sc = l >= 0 && p.scaling ? p.scaling[l] : 1.0f;
-    float top = 0.f;
-#pragma unroll
-    for (int s = 0; s < RS; ++s)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        h[s][e] = __fmul_rn(h[s][e], sc);
-        if constexpr (DT == 1) top = fmaxf(top, fabsf(h[s][e]));
-      }
-    // fp16: a power of two per token brings its h into the type's range (exact; undone on the
-    // sums), so that neither term overflows or loses bits. bf16 has fp32's range.
-    int ex = 0;
-    if constexpr (DT == 1) {
-      top = fmaxf(top, __shfl_xor(top, 16, 64));
-      top = fmaxf(top, __shfl_xor(top, 32, 64));
-      const int be = (int)(__float_as_uint(top) >> 23);
-      ex = be == 0 || be == 255 ? 0 : 127 + 14 - be;
-    }
-    vec hi[RS], lo[RS];
-#pragma unroll
-    for (int s = 0; s < RS; ++s)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float v = DT == 1 ? __builtin_ldexpf(h[s][e], ex) : h[s][e];
-        const one a = Half<DT>::round(v);
-        hi[s][e] = a;
-        lo[s][e] = Half<DT>::round(__builtin_isfinite((float)a) ? __fsub_rn(v, (float)a) : 0.f);
-      }
+    return v;
+  };
 
+  u32x4_t bv[D][NB][RS];
+  int held = -1;  // the adapter in bv[0]
+  Tile next = load_tile(tile);
+  for (; tile < last; ++tile) {
+    const Tile now = next;
+    if (tile + 1 < last) next = load_tile(tile + 1);
+    const int l = now.l;
     f32x4 d[NB];
 #pragma unroll
     for (int j = 0; j < NB; ++j) d[j] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -259,14 +449,15 @@ __global__ __launch_bounds__(kUpWaves * 64) void kq_adapter_up_kernel(const Adap
         if (a[k] < 0 || (k == 0 && a[0] == held)) continue;
         const uint16_t *bm = reinterpret_cast<const uint16_t *>(p.B) + (int64_t)a[k] * p.N * p.r;
 #pragma unroll
-        for (int j = 0; j < NB; ++j) {
-          const int n = min(n0 + (int)col + 4 * j, p.N - 1);  // columns past N: dropped below
+        for (int j = 0; j < NB; ++j)
 #pragma unroll
-          for (int s = 0; s < RS; ++s) {
-            const int kk = 32 * s + 8 * g;
-            bv[k][j][s] = kk < p.r ? *reinterpret_cast<const u32x4_t *>(bm + (int64_t)n * p.r + kk)
-                                   : u32x4_t{0, 0, 0, 0};
-          }
+          for (int s = 0; s < RS; ++s) bv[k][j][s] = *reinterpret_cast<const u32x4_t *>(bm + brow[j] + rank[s]);
+        if (p.r < 32 * RS) {  // ranks past r
+#pragma unroll
+          for (int s = 0; s < RS; ++s)
+            if (32 * s + 8 * g >= p.r)
+#pragma unroll
+              for (int j = 0; j < NB; ++j) bv[k][j][s] = u32x4_t{0, 0, 0, 0};
         }
       }
       held = a[0];
@@ -278,75 +469,93 @@ __global__ __launch_bounds__(kUpWaves * 64) void kq_adapter_up_kernel(const Adap
           f32x4 acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int s = 0; s < RS; ++s) {
-            acc = Half<DT>::mma(__builtin_bit_cast(vec, bv[k][j][s]), lo[s], acc);
-            acc = Half<DT>::mma(__builtin_bit_cast(vec, bv[k][j][s]), hi[s], acc);
+            acc = Half<DT>::mma(__builtin_bit_cast(vec, bv[k][j][s]), now.lo[s], acc);
+            acc = Half<DT>::mma(__builtin_bit_cast(vec, bv[k][j][s]), now.hi[s], acc);
           }
           if (l == a[k]) d[j] = acc;
         }
       }
     }
-    if (!live) continue;
-    // lane: columns nl + 4 j + r of token lr (N is a multiple of 8: a word is all in or all out)
+    // lane: columns 16 j + 4 g + 0..3 of token lr; the wave's own rows, in its program order
 #pragma unroll
-    for (int w = 0; w < kW; ++w) {
-      if (nl + 8 * w >= p.N) continue;
-      if (l >= 0) {
-        one v[8];
-        const one *b = reinterpret_cast<const one *>(&bs[w]);
+    for (int j = 0; j < NB; ++j) {
+      if constexpr (DT == 1)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float add = d[2 * w + e / 4][e % 4];
-          v[e] = Half<DT>::round(__fadd_rn((float)b[e], DT == 1 ? __builtin_ldexpf(add, -ex) : add));
-        }
-        bs[w] = *reinterpret_cast<const u32x4_t *>(v);
-      }
-      *reinterpret_cast<u32x4_t *>(reinterpret_cast<one *>(p.out) + t * p.ldo + nl + 8 * w) = bs[w];
+        for (int e = 0; e < 4; ++e) d[j][e] = __builtin_ldexpf(d[j][e], -now.ex);
+      *reinterpret_cast<f32x4 *>(mine + lr * kRow + 16 * j + 4 * g) = d[j];
     }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int w = 0; w < kPasses; ++w) {
+      const int row = tr + 64 / kLanes * w;
+      const int64_t t = tile * 16 + row;
+      const int lt = __shfl(l, row, 64);
+      u32x4_t o = now.base[w];
+      if (lt >= 0) {
+        const f32x4 *q = reinterpret_cast<const f32x4 *>(mine + row * kRow + 8 * (lane % kLanes));
+        const f32x4 add[2] = {q[0], q[1]};
+        const one *b = reinterpret_cast<const one *>(&now.base[w]);
+        one v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = Half<DT>::round(__fadd_rn((float)b[e], add[e / 4][e % 4]));
+        o = *reinterpret_cast<const u32x4_t *>(v);
+      }
+      if (in && t < p.T)
+        *reinterpret_cast<u32x4_t *>(reinterpret_cast<one *>(p.out) + t * p.ldo + nc) = o;
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
   }
 }
 
-// The first kernel's shape: blocks of 16 tokens per workgroup and its waves
-constexpr int64_t kWide = 4096;  // from this many tokens on: 32 tokens, 8 waves
-int down_tokens(int64_t T) { return T >= kWide ? 32 : 16; }
-int down_waves(int64_t T) { return T >= kWide ? 8 : 4; }
-
-// Parts of K: enough workgroups to fill the card where tokens are few, of 2 steps a wave at
-// least, and no more than the second kernel can add up at ease.
+// Parts of K: enough workgroups to fill the card where tokens are few, a step a wave at least,
+// and no more parts than the second kernel adds up at ease.
 int split_count(int64_t T, int64_t K) {
-  const int64_t tiles = (T + down_tokens(T) - 1) / down_tokens(T), steps = (K + 31) / 32;
-  int64_t s = (T >= kWide ? 256 : 512) / tiles;
-  const int64_t most = steps / (2 * down_waves(T));
-  if (s > most) s = most;
+  if (T >= kWide) return 1;
+  const int64_t tiles = (T + 15) / 16, steps = (K + kStep - 1) / kStep;
+  int64_t s = 512 / tiles;
+  if (s > steps / 4) s = steps / 4;
   return (int)(s < 1 ? 1 : s > 16 ? 16 : s);
 }
 
+// The first kernel's waves and each one's ring of LDS: three steps of a single adapter's rows
+// where 32 tokens go at once, two of several adapters' where 16 do (two workgroups then share a
+// compute unit's 160 KiB up to 64 ranks)
+template <int RB>
+struct Down {
+  static constexpr int kWideWaves = RB <= 2 ? 8 : RB <= 8 ? 4 : 2;
+  static constexpr int kWideRing = (RB <= 4 && RB != 2 ? 3 : 2) * (4 + 2 * RB) * 1024;
+  static constexpr int kD = RB == 1 ? 4 : RB == 2 ? 2 : 1;
+  static constexpr int kWaves = RB <= 8 ? 4 : 2;
+  static constexpr int kRing = 2 * (2 + kD * 2 * RB) * 1024;
+};
+
 template <int DT, int RB>
 hipError_t launch(AdapterArgs a, hipStream_t s) {
-  // adapters at a time and steps in flight: about 20 loads of a wave on their way
-  constexpr int D = RB == 1 ? 4 : RB <= 4 ? 2 : 1;
-  constexpr int U = RB == 1 ? 4 : RB == 2 ? 4 : RB <= 8 ? 2 : 1;
-  constexpr int UW = RB == 1 ? 8 : RB <= 4 ? 4 : RB == 8 ? 2 : 1;
-  const unsigned tiles = (unsigned)((a.T + down_tokens(a.T) - 1) / down_tokens(a.T));
-  constexpr int kWideWaves = RB < 16 ? 8 : 4;  // their parts in LDS: 128 KiB at most
-  const dim3 grid(tiles, (unsigned)a.splits);
-  if (a.T >= kWide)
-    hipLaunchKernelGGL((kq_adapter_down_kernel<DT, RB, 2, kWideWaves, 1, UW>), grid, dim3(kWideWaves * 64), 0,
-                       s, a);
-  else
-    hipLaunchKernelGGL((kq_adapter_down_kernel<DT, RB, 1, 4, D, U>), grid, dim3(4 * 64), 0, s, a);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  constexpr int RS = (RB + 1) / 2, NB = RS <= 2 ? 4 : 2, DU = RS == 1 ? 4 : RS <= 4 ? 2 : 1;
-  const int64_t t16 = (a.T + 15) / 16;
-  const int64_t cols = (a.N + 16 * NB * kUpWaves - 1) / (16 * NB * kUpWaves);
-  // some 2048 workgroups, each over a run of tiles whose adapters' B it keeps
+  typedef Down<RB> C;
+  constexpr int RS = (RB + 1) / 2, DU = RB <= 2 ? 4 : RB <= 8 ? 2 : 1, kCols = 16 * kUpBlocks<RS> * kUpWaves;
+  const int64_t t16 = (a.T + 15) / 16, cols = (a.N + kCols - 1) / kCols;
+  // some 2048 workgroups, each over a run of tiles whose adapter's B it keeps
   int64_t run = t16 * cols / 2048;
   if (run < 1) run = 1;
   if (run > 64) run = 64;
   while ((t16 + run - 1) / run > 65535) run *= 2;  // the grid's second dimension
   a.tiles_per_group = (int)run;
-  hipLaunchKernelGGL((kq_adapter_up_kernel<DT, RS, NB, DU>), dim3((unsigned)cols, (unsigned)((t16 + run - 1) / run)),
-                     dim3(kUpWaves * 64), 0, s, a);
+  const dim3 up((unsigned)cols, (unsigned)((t16 + run - 1) / run)), up_block(kUpWaves * 64);
+  if (a.T >= kWide) {
+    hipLaunchKernelGGL((kq_adapter_down_kernel<DT, RB, 2, C::kWideWaves, 1, C::kWideRing, true>),
+                       dim3((unsigned)((a.T + 31) / 32)), dim3(C::kWideWaves * 64), 0, s, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((kq_adapter_up_kernel<DT, RS, 1, true>), up, up_block, 0, s, a);
+  } else {
+    hipLaunchKernelGGL((kq_adapter_down_kernel<DT, RB, 1, C::kWaves, C::kD, C::kRing, false>),
+                       dim3((unsigned)t16, (unsigned)a.splits), dim3(C::kWaves * 64), 0, s, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((kq_adapter_up_kernel<DT, RS, DU, false>), up, up_block, 0, s, a);
+  }
   return hipGetLastError();
 }
 
@@ -364,7 +573,9 @@ constexpr int64_t kMax31 = 0x7FFFFFFF;
 bool off(const void *p, size_t a) { return ((uintptr_t)p % a) != 0; }
 
 int64_t workspace_bytes(int64_t T, int64_t K, int64_t r) {
-  const int64_t b = split_count(T, K) * T * ((r + 15) / 16 * 16) * 4;
+  // operands: 32 ranks of two 2-byte terms are the 128 bytes that 32 fp32 ranks take
+  const int64_t rb = r <= 16 ? 1 : r <= 32 ? 2 : r <= 64 ? 4 : r <= 128 ? 8 : 16, t16 = (T + 15) / 16 * 16;
+  const int64_t b = T >= kWide ? t16 * ((rb + 1) / 2 * 128 + 4) : split_count(T, K) * T * ((r + 15) / 16 * 16) * 4;
   return (b + 255) / 256 * 256;
 }
 
@@ -397,7 +608,8 @@ static kq_status adapter_add_impl(const void *x, int64_t ldx, const void *A, con
   if (T == 0 || N == 0) return KQ_OK;
   if (!x || !A || !B || !adapter || !out) return KQ_ERR_INVALID_ARG;
   if (ldx < K || (base && ldb < N) || ldo < N) return KQ_ERR_INVALID_ARG;
-  if (ldx > kMax31 || (base && ldb > kMax31) || ldo > kMax31) return KQ_ERR_UNSUPPORTED;
+  // 32 rows of x within 32 bits of byte offset
+  if (ldx > (1 << 25) || (base && ldb > kMax31) || ldo > kMax31) return KQ_ERR_UNSUPPORTED;
   if (off(x, 16) || off(A, 16) || off(B, 16) || off(base, 16) || off(out, 16) || ldx % 8 != 0 ||
       (base && ldb % 8 != 0) || ldo % 8 != 0 || off(adapter, 4) || off(scaling, 4))
     return KQ_ERR_ALIGNMENT;
@@ -411,10 +623,9 @@ static kq_status adapter_add_impl(const void *x, int64_t ldx, const void *A, con
   const int64_t need = workspace_bytes(T, K, r);
   if (!workspace || ws_bytes < (size_t)need) return KQ_ERR_WORKSPACE;
   if (off(workspace, 256)) return KQ_ERR_ALIGNMENT;
-  const int splits = split_count(T, K), steps = (int)((K + 31) / 32);
-  const AdapterArgs a = {x, A, B, base, adapter, scaling, out, static_cast<float *>(workspace), ldx, ldb,
-                         ldo, T, (int)K, (int)N, (int)r, (int)((r + 15) / 16 * 16), (int)L, splits,
-                         (steps + splits - 1) / splits, 1};
+  const int splits = split_count(T, K), steps = (int)((K + kStep - 1) / kStep);
+  const AdapterArgs a = {x, A, B, base, adapter, scaling, out, workspace, ldx, ldb, ldo, T, (int)K, (int)N,
+                         (int)r, (int)L, splits, (steps + splits - 1) / splits, 1};
   hipStream_t s = static_cast<hipStream_t>(stream);
   const hipError_t e = dtype == KQ_BF16 ? dispatch<0>(a, s) : dispatch<1>(a, s);
   return e == hipSuccess ? KQ_OK : KQ_ERR_HIP;
