@@ -266,7 +266,7 @@ __global__ __launch_bounds__(WAVES * 64) void kq_adapter_down_kernel(const Adapt
                                      4 * g) = v;
       }
   };
-  while (left) {
+  for (int group = 0; left; ++group) {
     int a[D], n = 0;
 #pragma unroll
     for (int d = 0; d < D; ++d) {
@@ -274,6 +274,7 @@ __global__ __launch_bounds__(WAVES * 64) void kq_adapter_down_kernel(const Adapt
       a[d] = next < 0 ? a[0] : next;  // a short group's rest: its first adapter again, dropped
       n += next >= 0;
     }
+    if (group % (int)gridDim.z != (int)blockIdx.z) continue;  // another workgroup's
     unsigned char *ring = s_mem + wave * RING;
     if (n == 1) {
       f32x4 acc[1][RB][TF];
@@ -348,11 +349,13 @@ __global__ __launch_bounds__(kUpWaves * 64) void kq_adapter_up_kernel(const Adap
   typedef typename Half<DT>::one one;
   constexpr int NB = kUpBlocks<RS>, kRow = 16 * NB + 4;  // floats of a row in LDS: all banks in turn
   constexpr int kLanes = 2 * NB, kPasses = NB / 2;       // lanes of a row of base and out
+  constexpr int kHRow = 32 * RS + 4;
   __shared__ __align__(16) float s_out[kUpWaves][16 * kRow];
+  __shared__ __align__(16) float s_h[OPERANDS ? 1 : 2][OPERANDS ? 4 : 16 * kHRow];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int g = lane >> 4, lr = lane & 15;
   const int n0 = (int)(blockIdx.x * kUpWaves + wave) * 16 * NB;
-  if (n0 >= p.N) return;  // whole waves; there is no barrier here
+  if (OPERANDS && n0 >= p.N) return;  // whole waves; there is no barrier then
   int64_t tile = (int64_t)blockIdx.y * p.tiles_per_group;
   const int64_t tiles = (p.T + 15) / 16, last = min(tile + p.tiles_per_group, tiles);
   uint32_t brow[NB];  // this lane's rows of B, in values; columns past N: dropped below
@@ -372,8 +375,7 @@ __global__ __launch_bounds__(kUpWaves * 64) void kq_adapter_up_kernel(const Adap
   };
   auto load_tile = [&](int64_t tile) {
     Tile v;
-    const int64_t t = tile * 16 + lr, tc = t < p.T ? t : p.T - 1;
-    v.l = token_adapter(p, t);
+    v.l = token_adapter(p, tile * 16 + lr);
     v.ex = 0;
 #pragma unroll
     for (int w = 0; w < kPasses; ++w) {
@@ -391,51 +393,49 @@ __global__ __launch_bounds__(kUpWaves * 64) void kq_adapter_up_kernel(const Adap
       }
       if constexpr (DT == 1)
         v.ex = (reinterpret_cast<const int *>(reinterpret_cast<const vec *>(p.ws) + tiles * (RS * 2 * 64)))[tile * 16 + lr];
-    } else {
-      // h of a token without an adapter is what the workspace holds, and dropped
-      const int r16 = round16(p.r);
-      const float *q = reinterpret_cast<const float *>(p.ws) + tc * r16;
-      constexpr int kAt = RS <= 4 ? 8 / RS : 1;  // parts on their way at a time
-      float h[RS][8];
-#pragma unroll
-      for (int s = 0; s < RS; ++s)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) h[s][e] = 0.f;
-      for (int i = 0; i < p.splits; i += kAt) {
-        f32x4 w[kAt][RS][2];
-#pragma unroll
-        for (int k = 0; k < kAt; ++k) {
-          const float *qi = q + (int64_t)min(i + k, p.splits - 1) * p.T * r16;
-#pragma unroll
-          for (int s = 0; s < RS; ++s)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) w[k][s][e] = *reinterpret_cast<const f32x4 *>(qi + rank[s] + 4 * e);
-        }
-#pragma unroll
-        for (int k = 0; k < kAt; ++k)
-          if (i + k < p.splits)
-#pragma unroll
-            for (int s = 0; s < RS; ++s)
-#pragma unroll
-              for (int e = 0; e < 8; ++e) h[s][e] += w[k][s][e / 4][e % 4];
-      }
-      const float sc = v.l >= 0 && p.scaling ? p.scaling[v.l] : 1.0f;
-#pragma unroll
-      for (int s = 0; s < RS; ++s)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) h[s][e] = 32 * s + 8 * g < p.r ? __fmul_rn(h[s][e], sc) : 0.f;
-      v.ex = two_terms<DT, RS>(h, v.hi, v.lo);
     }
     return v;
+  };
+  // The parts' sums, by the whole workgroup: 16 tokens of r16 ranks stand one behind another in
+  // each part. What a token without an adapter has there is dropped.
+  auto sum_parts = [&](int64_t tile, float *to) {
+    const int r16 = round16(p.r), values = (int)min((int64_t)16, p.T - tile * 16) * r16;
+    const float *q = reinterpret_cast<const float *>(p.ws) + tile * 16 * r16;
+    const int64_t part = p.T * r16;
+    for (int i = threadIdx.x; i < values; i += kUpWaves * 64) {
+      float h = 0.f;
+      int k = 0;
+      for (; k + 4 <= p.splits; k += 4) {
+        const float a = q[k * part + i], b = q[(k + 1) * part + i], c = q[(k + 2) * part + i], d = q[(k + 3) * part + i];
+        h = ((h + a) + b) + c;
+        h += d;
+      }
+      for (; k < p.splits; ++k) h += q[k * part + i];
+      to[i / r16 * kHRow + i % r16] = h;
+    }
   };
 
   u32x4_t bv[D][NB][RS];
   int held = -1;  // the adapter in bv[0]
   Tile next = load_tile(tile);
-  for (; tile < last; ++tile) {
-    const Tile now = next;
+  for (int turn = 0; tile < last; ++tile, turn ^= 1) {
+    Tile now = next;
+    if constexpr (!OPERANDS) sum_parts(tile, s_h[turn]);
     if (tile + 1 < last) next = load_tile(tile + 1);
     const int l = now.l;
+    if constexpr (!OPERANDS) {
+      lds_barrier();  // two buffers in turn: one barrier per tile
+      const float sc = l >= 0 && p.scaling ? p.scaling[l] : 1.0f;
+      float h[RS][8];
+#pragma unroll
+      for (int s = 0; s < RS; ++s) {
+        const f32x4 *q = reinterpret_cast<const f32x4 *>(s_h[turn] + lr * kHRow + rank[s]);
+        const f32x4 v[2] = {q[0], q[1]};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) h[s][e] = l >= 0 && 32 * s + 8 * g < p.r ? __fmul_rn(v[e / 4][e % 4], sc) : 0.f;
+      }
+      now.ex = two_terms<DT, RS>(h, now.hi, now.lo);
+    }
     f32x4 d[NB];
 #pragma unroll
     for (int j = 0; j < NB; ++j) d[j] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -516,7 +516,7 @@ int split_count(int64_t T, int64_t K) {
   const int64_t tiles = (T + 15) / 16, steps = (K + kStep - 1) / kStep;
   int64_t s = 512 / tiles;
   if (s > steps / 4) s = steps / 4;
-  return (int)(s < 1 ? 1 : s > 16 ? 16 : s);
+  return (int)(s < 1 ? 1 : s > 8 ? 8 : s);
 }
 
 // The first kernel's waves and each one's ring of LDS: three steps of a single adapter's rows
@@ -550,8 +550,11 @@ hipError_t launch(AdapterArgs a, hipStream_t s) {
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL((kq_adapter_up_kernel<DT, RS, 1, true>), up, up_block, 0, s, a);
   } else {
+    // a decode batch's tile may have 16 adapters: workgroups share them out, up to some 2048
+    const int64_t most = (a.T < 16 ? a.T + C::kD - 1 : 16) / C::kD, room = 2048 / (t16 * a.splits);
+    const unsigned groups = (unsigned)(room < 1 ? 1 : room < most ? room : most);
     hipLaunchKernelGGL((kq_adapter_down_kernel<DT, RB, 1, C::kWaves, C::kD, C::kRing, false>),
-                       dim3((unsigned)t16, (unsigned)a.splits), dim3(C::kWaves * 64), 0, s, a);
+                       dim3((unsigned)t16, (unsigned)a.splits, groups), dim3(C::kWaves * 64), 0, s, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL((kq_adapter_up_kernel<DT, RS, DU, false>), up, up_block, 0, s, a);
