@@ -340,14 +340,11 @@ constexpr int kUpWaves = 4;
 // base and out: in the product's own layout every lane is a row of its own, and each 16 bytes a
 // memory access of its own. A tile's base and h are on their way while the one before it is
 // computed. OPERANDS: what lies between the kernels, see above.
-template <int RS>
-constexpr int kUpBlocks = RS <= 2 ? 4 : 2;  // blocks of 16 columns per wave: their B in registers
-
-template <int DT, int RS, int D, bool OPERANDS>
+template <int DT, int RS, int NB, int D, bool OPERANDS>
 __global__ __launch_bounds__(kUpWaves * 64) void kq_adapter_up_kernel(const AdapterArgs p) {
   typedef typename Half<DT>::vec vec;
   typedef typename Half<DT>::one one;
-  constexpr int NB = kUpBlocks<RS>, kRow = 16 * NB + 4;  // floats of a row in LDS: all banks in turn
+  constexpr int kRow = 16 * NB + 4;                      // floats of a row in LDS: all banks in turn
   constexpr int kLanes = 2 * NB, kPasses = NB / 2;       // lanes of a row of base and out
   constexpr int kHRow = 32 * RS + 4;
   __shared__ __align__(16) float s_out[kUpWaves][16 * kRow];
@@ -381,8 +378,11 @@ __global__ __launch_bounds__(kUpWaves * 64) void kq_adapter_up_kernel(const Adap
     for (int w = 0; w < kPasses; ++w) {
       const int64_t tb = tile * 16 + tr + 64 / kLanes * w;
       v.base[w] = u32x4_t{0, 0, 0, 0};
-      if (p.base && in && tb < p.T)
-        v.base[w] = *reinterpret_cast<const u32x4_t *>(reinterpret_cast<const one *>(p.base) + tb * p.ldb + nc);
+      if (p.base && in && tb < p.T) {
+        const auto *b = reinterpret_cast<const u32x4_t *>(reinterpret_cast<const one *>(p.base) + tb * p.ldb + nc);
+        // many tokens: base and out pass once and would push h and B out of the caches
+        v.base[w] = OPERANDS ? __builtin_nontemporal_load(b) : *b;
+      }
     }
     if constexpr (OPERANDS) {
       const vec *o = reinterpret_cast<const vec *>(p.ws) + tile * (RS * 2 * 64) + lane;
@@ -417,15 +417,35 @@ __global__ __launch_bounds__(kUpWaves * 64) void kq_adapter_up_kernel(const Adap
 
   u32x4_t bv[D][NB][RS];
   int held = -1;  // the adapter in bv[0]
+  auto load_b = [&](const int (&a)[D]) {
+#pragma unroll
+    for (int k = 0; k < D; ++k) {
+      if (a[k] < 0 || (k == 0 && a[0] == held)) continue;
+      const uint16_t *bm = reinterpret_cast<const uint16_t *>(p.B) + (int64_t)a[k] * p.N * p.r;
+#pragma unroll
+      for (int j = 0; j < NB; ++j)
+#pragma unroll
+        for (int s = 0; s < RS; ++s) bv[k][j][s] = *reinterpret_cast<const u32x4_t *>(bm + brow[j] + rank[s]);
+    }
+    held = a[0];
+  };
+  const bool ragged = p.r < 32 * RS;  // ranks past r: 0 on both sides
   Tile next = load_tile(tile);
   for (int turn = 0; tile < last; ++tile, turn ^= 1) {
     Tile now = next;
+    const int l = now.l;
+    // the first adapters' B before anything that waits
+    unsigned long long left = __ballot(l >= 0) & 0xFFFFull;
+    const bool any = left != 0;
+    int a[D];
+#pragma unroll
+    for (int k = 0; k < D; ++k) a[k] = next_adapter(left, l);
+    if (any) load_b(a);
     if constexpr (!OPERANDS) sum_parts(tile, s_h[turn]);
     if (tile + 1 < last) next = load_tile(tile + 1);
-    const int l = now.l;
     if constexpr (!OPERANDS) {
-      lds_barrier();  // two buffers in turn: one barrier per tile
       const float sc = l >= 0 && p.scaling ? p.scaling[l] : 1.0f;
+      lds_barrier();  // two buffers in turn: one barrier per tile
       float h[RS][8];
 #pragma unroll
       for (int s = 0; s < RS; ++s) {
@@ -439,28 +459,7 @@ __global__ __launch_bounds__(kUpWaves * 64) void kq_adapter_up_kernel(const Adap
     f32x4 d[NB];
 #pragma unroll
     for (int j = 0; j < NB; ++j) d[j] = f32x4{0.f, 0.f, 0.f, 0.f};
-    unsigned long long left = __ballot(l >= 0) & 0xFFFFull;
-    while (left) {
-      int a[D];
-#pragma unroll
-      for (int k = 0; k < D; ++k) a[k] = next_adapter(left, l);
-#pragma unroll
-      for (int k = 0; k < D; ++k) {
-        if (a[k] < 0 || (k == 0 && a[0] == held)) continue;
-        const uint16_t *bm = reinterpret_cast<const uint16_t *>(p.B) + (int64_t)a[k] * p.N * p.r;
-#pragma unroll
-        for (int j = 0; j < NB; ++j)
-#pragma unroll
-          for (int s = 0; s < RS; ++s) bv[k][j][s] = *reinterpret_cast<const u32x4_t *>(bm + brow[j] + rank[s]);
-        if (p.r < 32 * RS) {  // ranks past r
-#pragma unroll
-          for (int s = 0; s < RS; ++s)
-            if (32 * s + 8 * g >= p.r)
-#pragma unroll
-              for (int j = 0; j < NB; ++j) bv[k][j][s] = u32x4_t{0, 0, 0, 0};
-        }
-      }
-      held = a[0];
+    while (any) {
 #pragma unroll
       for (int k = 0; k < D; ++k) {
         if (a[k] < 0) continue;
@@ -469,12 +468,18 @@ __global__ __launch_bounds__(kUpWaves * 64) void kq_adapter_up_kernel(const Adap
           f32x4 acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int s = 0; s < RS; ++s) {
-            acc = Half<DT>::mma(__builtin_bit_cast(vec, bv[k][j][s]), now.lo[s], acc);
-            acc = Half<DT>::mma(__builtin_bit_cast(vec, bv[k][j][s]), now.hi[s], acc);
+            u32x4_t b = bv[k][j][s];
+            if (ragged) b = 32 * s + 8 * g < p.r ? b : u32x4_t{0, 0, 0, 0};
+            acc = Half<DT>::mma(__builtin_bit_cast(vec, b), now.lo[s], acc);
+            acc = Half<DT>::mma(__builtin_bit_cast(vec, b), now.hi[s], acc);
           }
           if (l == a[k]) d[j] = acc;
         }
       }
+      if (!left) break;
+#pragma unroll
+      for (int k = 0; k < D; ++k) a[k] = next_adapter(left, l);
+      load_b(a);
     }
     // lane: columns 16 j + 4 g + 0..3 of token lr; the wave's own rows, in its program order
 #pragma unroll
@@ -501,8 +506,11 @@ __global__ __launch_bounds__(kUpWaves * 64) void kq_adapter_up_kernel(const Adap
         for (int e = 0; e < 8; ++e) v[e] = Half<DT>::round(__fadd_rn((float)b[e], add[e / 4][e % 4]));
         o = *reinterpret_cast<const u32x4_t *>(v);
       }
-      if (in && t < p.T)
-        *reinterpret_cast<u32x4_t *>(reinterpret_cast<one *>(p.out) + t * p.ldo + nc) = o;
+      if (in && t < p.T) {
+        auto *to = reinterpret_cast<u32x4_t *>(reinterpret_cast<one *>(p.out) + t * p.ldo + nc);
+        if constexpr (OPERANDS) __builtin_nontemporal_store(o, to);
+        else *to = o;
+      }
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
@@ -524,42 +532,49 @@ int split_count(int64_t T, int64_t K) {
 // compute unit's 160 KiB up to 64 ranks)
 template <int RB>
 struct Down {
-  static constexpr int kWideWaves = RB <= 2 ? 8 : RB <= 8 ? 4 : 2;
-  static constexpr int kWideRing = (RB <= 4 && RB != 2 ? 3 : 2) * (4 + 2 * RB) * 1024;
+  static constexpr int kWideWaves = RB == 1 ? 8 : RB <= 8 ? 4 : 2;
+  static constexpr int kWideD = RB <= 4 ? 2 : 1;  // a tile where two prompts meet has two
+  static constexpr int kWideRing = 2 * (4 + kWideD * 2 * RB) * 1024;
   static constexpr int kD = RB == 1 ? 4 : RB == 2 ? 2 : 1;
   static constexpr int kWaves = RB <= 8 ? 4 : 2;
   static constexpr int kRing = 2 * (2 + kD * 2 * RB) * 1024;
 };
 
-template <int DT, int RB>
-hipError_t launch(AdapterArgs a, hipStream_t s) {
-  typedef Down<RB> C;
-  constexpr int RS = (RB + 1) / 2, DU = RB <= 2 ? 4 : RB <= 8 ? 2 : 1, kCols = 16 * kUpBlocks<RS> * kUpWaves;
+template <int DT, int RS, int NB, int D, bool OPERANDS>
+hipError_t launch_up(AdapterArgs a, hipStream_t s) {
+  constexpr int kCols = 16 * NB * kUpWaves;
   const int64_t t16 = (a.T + 15) / 16, cols = (a.N + kCols - 1) / kCols;
-  // some 2048 workgroups, each over a run of tiles whose adapter's B it keeps
-  int64_t run = t16 * cols / 2048;
+  // some 4096 workgroups, each over a run of tiles whose adapter's B it keeps
+  int64_t run = t16 * cols / 4096;
   if (run < 1) run = 1;
   if (run > 64) run = 64;
   while ((t16 + run - 1) / run > 65535) run *= 2;  // the grid's second dimension
   a.tiles_per_group = (int)run;
-  const dim3 up((unsigned)cols, (unsigned)((t16 + run - 1) / run)), up_block(kUpWaves * 64);
+  hipLaunchKernelGGL((kq_adapter_up_kernel<DT, RS, NB, D, OPERANDS>),
+                     dim3((unsigned)cols, (unsigned)((t16 + run - 1) / run)), dim3(kUpWaves * 64), 0, s, a);
+  return hipGetLastError();
+}
+
+template <int DT, int RB>
+hipError_t launch(AdapterArgs a, hipStream_t s) {
+  typedef Down<RB> C;
+  constexpr int RS = (RB + 1) / 2;
   if (a.T >= kWide) {
-    hipLaunchKernelGGL((kq_adapter_down_kernel<DT, RB, 2, C::kWideWaves, 1, C::kWideRing, true>),
+    hipLaunchKernelGGL((kq_adapter_down_kernel<DT, RB, 2, C::kWideWaves, C::kWideD, C::kWideRing, true>),
                        dim3((unsigned)((a.T + 31) / 32)), dim3(C::kWideWaves * 64), 0, s, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((kq_adapter_up_kernel<DT, RS, 1, true>), up, up_block, 0, s, a);
-  } else {
-    // a decode batch's tile may have 16 adapters: workgroups share them out, up to some 2048
-    const int64_t most = (a.T < 16 ? a.T + C::kD - 1 : 16) / C::kD, room = 2048 / (t16 * a.splits);
-    const unsigned groups = (unsigned)(room < 1 ? 1 : room < most ? room : most);
-    hipLaunchKernelGGL((kq_adapter_down_kernel<DT, RB, 1, C::kWaves, C::kD, C::kRing, false>),
-                       dim3((unsigned)t16, (unsigned)a.splits, groups), dim3(C::kWaves * 64), 0, s, a);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((kq_adapter_up_kernel<DT, RS, DU, false>), up, up_block, 0, s, a);
+    return launch_up<DT, RS, RS <= 2 ? 4 : 2, 1, true>(a, s);
   }
-  return hipGetLastError();
+  // a decode batch's tile may have 16 adapters: workgroups share them out, up to some 1024
+  const int64_t t16 = (a.T + 15) / 16;
+  const int64_t most = (a.T < 16 ? a.T + C::kD - 1 : 16) / C::kD, room = 1024 / (t16 * a.splits);
+  const unsigned groups = (unsigned)(room < 1 ? 1 : room < most ? room : most);
+  hipLaunchKernelGGL((kq_adapter_down_kernel<DT, RB, 1, C::kWaves, C::kD, C::kRing, false>),
+                     dim3((unsigned)t16, (unsigned)a.splits, groups), dim3(C::kWaves * 64), 0, s, a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  return launch_up<DT, RS, RS <= 2 ? 4 : 2, RB <= 2 ? 4 : RB <= 8 ? 2 : 1, false>(a, s);
 }
 
 template <int DT>
