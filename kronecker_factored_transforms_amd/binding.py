@@ -304,18 +304,6 @@ def _elsewhere(device, stream):
                 yield
 
 
-_HERE_ALREADY = contextlib.nullcontext()
-
-
-def _on(x, stream):
-    """Context in which x's device is current and `stream` (None: its current one) takes the
-    launches and owns the allocations."""
-    import torch
-    if stream is None and torch.cuda.current_device() == x.get_device():
-        return _HERE_ALREADY
-    return _elsewhere(x.device, stream)
-
-
 def _current(index) -> int:
     """Handle of device `index`'s current stream."""
     import torch
@@ -333,16 +321,23 @@ def _need_rows(name, t, shape, dtype, index):
     if t.dtype is dtype and t.shape == shape and t.get_device() == index:
         rows, width = shape
         ld, step = t.stride()
-        if rows <= 1 and (step == 1 or width <= 1):
-            return width
-        if ld >= width and (step == 1 or width <= 1):
-            return ld
+        if step == 1 or width <= 1:
+            if rows <= 1:
+                return width
+            if ld >= width:
+                return ld
     raise ValueError(f"{name} must be a {list(shape)} {dtype} tensor with unit column stride on GPU {index}")
 
 
 def _need_whole(name, t, shape, dtype, index):
     if not (t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous()):
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {list(shape)} on GPU {index}")
+
+
+def _here(index, stream):
+    """Whether GPU `index` is current and its current stream is the one to launch on."""
+    import torch
+    return stream is None and torch.cuda.current_device() == index
 
 
 class NormQuant(NamedTuple):
@@ -367,7 +362,11 @@ def rmsnorm_quant(x, weight, residual=None, eps=1e-5, alpha=math.inf, scale_dtyp
     residual themselves, out.normed may be x itself."""
     import torch
     _need(x.dim() == 2 and x.is_cuda, "x must be a [T, n] GPU tensor")
-    dt, shape, dev = x.dtype, x.shape, x.get_device()
+    dev = x.get_device()
+    if not _here(dev, stream):
+        with _elsewhere(x.device, stream):
+            return rmsnorm_quant(x, weight, residual, eps, alpha, scale_dtype, codes, normed, out)
+    dt, shape = x.dtype, x.shape
     T, n = shape
     dtc = KQ_BF16 if dt is torch.bfloat16 else KQ_FP16 if dt is torch.float16 else KQ_FP32
     _need(dtc != KQ_FP32 or dt is torch.float32, "x must be bf16, fp16 or fp32")
@@ -380,38 +379,36 @@ def rmsnorm_quant(x, weight, residual=None, eps=1e-5, alpha=math.inf, scale_dtyp
     q = s = r = y = None
     pr = pro = py = pq = ps = None
     ldr = ldro = ldy = n
+    o = _ALL_NEW if out is None else out
     if residual is not None:
         ldr, pr = _need_rows("residual", residual, shape, dt, dev), residual.data_ptr()
-    o = _ALL_NEW if out is None else out
-    with _on(x, stream):
-        if codes:
-            sdt = torch.float16 if sdc == KQ_FP16 else torch.float32
-            q, s = o.codes, o.scales
-            if q is None:
-                q = x.new_empty(shape, dtype=torch.uint8)
-            else:
-                _need_whole("out.codes", q, shape, torch.uint8, dev)
-            if s is None:
-                s = x.new_empty(T, dtype=sdt)
-            else:
-                _need_whole("out.scales", s, (T,), sdt, dev)
-            pq, ps = q.data_ptr(), s.data_ptr()
-        if residual is not None:
-            r = o.residual
-            if r is None:
-                r = x.new_empty(shape)
-            else:
-                ldro = _need_rows("out.residual", r, shape, dt, dev)
-            pro = r.data_ptr()
-        if normed:
-            y = o.normed
-            if y is None:
-                y = x.new_empty(shape)
-            else:
-                ldy = _need_rows("out.normed", y, shape, dt, dev)
-            py = y.data_ptr()
-        st = lib().kq_rmsnorm_quant(x.data_ptr(), ldx, pr, ldr, weight.data_ptr(), T, n, dtc, eps, alpha,
-                                    sdc, pro, ldro, py, ldy, pq, ps, _current(dev))
+        r = o.residual
+        if r is None:
+            r = x.new_empty(shape)
+        else:
+            ldro = _need_rows("out.residual", r, shape, dt, dev)
+        pro = r.data_ptr()
+    if codes:
+        sdt = torch.float16 if sdc == KQ_FP16 else torch.float32
+        q, s = o.codes, o.scales
+        if q is None:
+            q = x.new_empty(shape, dtype=torch.uint8)
+        else:
+            _need_whole("out.codes", q, shape, torch.uint8, dev)
+        if s is None:
+            s = x.new_empty(T, dtype=sdt)
+        else:
+            _need_whole("out.scales", s, (T,), sdt, dev)
+        pq, ps = q.data_ptr(), s.data_ptr()
+    if normed:
+        y = o.normed
+        if y is None:
+            y = x.new_empty(shape)
+        else:
+            ldy = _need_rows("out.normed", y, shape, dt, dev)
+        py = y.data_ptr()
+    st = lib().kq_rmsnorm_quant(x.data_ptr(), ldx, pr, ldr, weight.data_ptr(), T, n, dtc, eps, alpha,
+                                sdc, pro, ldro, py, ldy, pq, ps, _current(dev))
     if st != KQ_OK:
         _check(st, "kq_rmsnorm_quant")
     return NormQuant(q, s, r, y)
@@ -427,16 +424,19 @@ def grouped_gemm(xq, sx, wq, sw, offsets, rows=None, bits=4, out_dtype="fp32", o
     have to hold something."""
     import torch
     _need(xq.dim() == 2 and xq.is_cuda, "xq must be a [T, bytes] GPU tensor")
+    dev = xq.get_device()
+    if not _here(dev, stream):
+        with _elsewhere(xq.device, stream):
+            return grouped_gemm(xq, sx, wq, sw, offsets, rows, bits, out_dtype, out)
     _need(wq.dim() == 3 and wq.shape[0] >= 1, "wq must be [E, N, bytes]")
     _need(bits == 4 or bits == 8, "bits must be 4 or 8")
-    dev = xq.get_device()
     T, width = xq.shape
     E, N, wide = wq.shape
     _need(width == wide and width >= 1, "xq's and wq's rows of codes differ in length")
     ldx = _need_rows("xq", xq, (T, width), torch.uint8, dev)
     lde, ldw, step = wq.stride()
     _need(wq.dtype is torch.uint8 and wq.get_device() == dev and (step == 1 or wide == 1),
-          f"wq must be uint8 with unit stride in a row, on GPU {dev}")
+          "wq must be uint8 with unit stride in a row, on xq's GPU")
     if N <= 1:
         ldw = wide
     if E <= 1:
@@ -455,15 +455,14 @@ def grouped_gemm(xq, sx, wq, sw, offsets, rows=None, bits=4, out_dtype="fp32", o
         prows = rows.data_ptr()
     odc = _dtype_code(out_dtype)
     odt = torch.bfloat16 if odc == KQ_BF16 else torch.float16 if odc == KQ_FP16 else torch.float32
-    with _on(xq, stream):
-        if out is None:
-            out, ldo = sx.new_empty((R, N), dtype=odt), N
-        else:
-            ldo = _need_rows("out", out, (R, N), odt, dev)
-        st = lib().kq_grouped_gemm(xq.data_ptr(), ldx, sx.data_ptr(), T, prows, R, wq.data_ptr(), ldw, lde,
-                                   sw.data_ptr(), N, width * 8 // bits, E, offsets.data_ptr(), bits,
-                                   KQ_FP16 if sdt is torch.float16 else KQ_FP32, odc, out.data_ptr(), ldo,
-                                   _current(dev))
+    if out is None:
+        out, ldo = sx.new_empty((R, N), dtype=odt), N
+    else:
+        ldo = _need_rows("out", out, (R, N), odt, dev)
+    st = lib().kq_grouped_gemm(xq.data_ptr(), ldx, sx.data_ptr(), T, prows, R, wq.data_ptr(), ldw, lde,
+                               sw.data_ptr(), N, width * 8 // bits, E, offsets.data_ptr(), bits,
+                               KQ_FP16 if sdt is torch.float16 else KQ_FP32, odc, out.data_ptr(), ldo,
+                               _current(dev))
     if st != KQ_OK:
         _check(st, "kq_grouped_gemm")
     return out
@@ -480,8 +479,12 @@ def adapter_add(x, A, B, adapter, base=None, scaling=None, out=None, workspace=N
     allocated here when not given."""
     import torch
     _need(x.dim() == 2 and x.is_cuda, "x must be a [T, K] GPU tensor")
+    dev = x.get_device()
+    if not _here(dev, stream):
+        with _elsewhere(x.device, stream):
+            return adapter_add(x, A, B, adapter, base, scaling, out, workspace)
     _need(A.dim() == 3 and B.dim() == 3, "A must be [L, r, K] and B [L, N, r]")
-    dev, dt = x.get_device(), x.dtype
+    dt = x.dtype
     _need(dt is torch.bfloat16 or dt is torch.float16, "x must be bf16 or fp16")
     T, K = x.shape
     L, r, _ = A.shape
@@ -491,27 +494,25 @@ def adapter_add(x, A, B, adapter, base=None, scaling=None, out=None, workspace=N
     _need_whole("B", B, (L, N, r), dt, dev)
     _need_whole("adapter", adapter, (T,), torch.int32, dev)
     ps = pb = None
-    ldb = N
+    ldb = ldo = N
     if scaling is not None:
         _need_whole("scaling", scaling, (L,), torch.float32, dev)
         ps = scaling.data_ptr()
     if base is not None:
         ldb, pb = _need_rows("base", base, (T, N), dt, dev), base.data_ptr()
-    with _on(x, stream):
-        if out is None:
-            out, ldo = x.new_empty((T, N)), N
-        else:
-            ldo = _need_rows("out", out, (T, N), dt, dev)
-        need = kq_adapter_workspace_size(T, K, r)
-        if workspace is None:
-            workspace = x.new_empty(need, dtype=torch.uint8)
-        else:
-            _need(workspace.dtype is torch.uint8 and workspace.get_device() == dev
-                  and workspace.is_contiguous() and workspace.numel() >= need,
-                  f"workspace must be {need} contiguous bytes on GPU {dev}")
-        st = lib().kq_adapter_add(x.data_ptr(), ldx, A.data_ptr(), B.data_ptr(), adapter.data_ptr(), ps, pb, ldb,
-                                  T, K, N, r, L, KQ_BF16 if dt is torch.bfloat16 else KQ_FP16, out.data_ptr(),
-                                  ldo, workspace.data_ptr(), workspace.numel(), _current(dev))
+    if out is None:
+        out = x.new_empty((T, N))
+    else:
+        ldo = _need_rows("out", out, (T, N), dt, dev)
+    need = kq_adapter_workspace_size(T, K, r)
+    if workspace is None:
+        workspace = x.new_empty(need, dtype=torch.uint8)
+    elif not (workspace.dtype is torch.uint8 and workspace.get_device() == dev
+              and workspace.is_contiguous() and workspace.numel() >= need):
+        raise ValueError(f"workspace must be {need} contiguous bytes on GPU {dev}")
+    st = lib().kq_adapter_add(x.data_ptr(), ldx, A.data_ptr(), B.data_ptr(), adapter.data_ptr(), ps, pb, ldb,
+                              T, K, N, r, L, KQ_BF16 if dt is torch.bfloat16 else KQ_FP16, out.data_ptr(),
+                              ldo, workspace.data_ptr(), workspace.numel(), _current(dev))
     if st != KQ_OK:
         _check(st, "kq_adapter_add")
     return out

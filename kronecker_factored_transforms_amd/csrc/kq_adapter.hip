@@ -365,36 +365,33 @@ __global__ __launch_bounds__(kUpWaves * 64) void kq_adapter_up_kernel(const Adap
   const bool in = nc < p.N;  // N is a multiple of 8: a word is all in or all out
   float *mine = s_out[wave];
 
-  struct Tile {
-    int l, ex;
-    u32x4_t base[kPasses];
-    vec hi[RS], lo[RS];
-  };
-  auto load_tile = [&](int64_t tile) {
-    Tile v;
-    v.l = token_adapter(p, tile * 16 + lr);
-    v.ex = 0;
+  u32x4_t base[2][kPasses];  // of this tile and the next
+  auto load_base = [&](int64_t tile, u32x4_t (&to)[kPasses]) {
 #pragma unroll
     for (int w = 0; w < kPasses; ++w) {
-      const int64_t tb = tile * 16 + tr + 64 / kLanes * w;
-      v.base[w] = u32x4_t{0, 0, 0, 0};
-      if (p.base && in && tb < p.T) {
-        const auto *b = reinterpret_cast<const u32x4_t *>(reinterpret_cast<const one *>(p.base) + tb * p.ldb + nc);
+      const int64_t t = tile * 16 + tr + 64 / kLanes * w;
+      to[w] = u32x4_t{0, 0, 0, 0};
+      if (p.base && in && t < p.T) {
+        const auto *b = reinterpret_cast<const u32x4_t *>(reinterpret_cast<const one *>(p.base) + t * p.ldb + nc);
         // many tokens: base and out pass once and would push h and B out of the caches
-        v.base[w] = OPERANDS ? __builtin_nontemporal_load(b) : *b;
+        to[w] = OPERANDS ? __builtin_nontemporal_load(b) : *b;
       }
     }
+  };
+  int l, ex = 0;
+  vec hi[RS], lo[RS];
+  auto load_h = [&](int64_t tile) {
+    l = token_adapter(p, tile * 16 + lr);
     if constexpr (OPERANDS) {
       const vec *o = reinterpret_cast<const vec *>(p.ws) + tile * (RS * 2 * 64) + lane;
 #pragma unroll
       for (int s = 0; s < RS; ++s) {
-        v.hi[s] = o[(2 * s) * 64];
-        v.lo[s] = o[(2 * s + 1) * 64];
+        hi[s] = o[(2 * s) * 64];
+        lo[s] = o[(2 * s + 1) * 64];
       }
       if constexpr (DT == 1)
-        v.ex = (reinterpret_cast<const int *>(reinterpret_cast<const vec *>(p.ws) + tiles * (RS * 2 * 64)))[tile * 16 + lr];
+        ex = (reinterpret_cast<const int *>(reinterpret_cast<const vec *>(p.ws) + tiles * (RS * 2 * 64)))[tile * 16 + lr];
     }
-    return v;
   };
   // The parts' sums, by the whole workgroup: 16 tokens of r16 ranks stand one behind another in
   // each part. What a token without an adapter has there is dropped.
@@ -430,10 +427,9 @@ __global__ __launch_bounds__(kUpWaves * 64) void kq_adapter_up_kernel(const Adap
     held = a[0];
   };
   const bool ragged = p.r < 32 * RS;  // ranks past r: 0 on both sides
-  Tile next = load_tile(tile);
+  load_h(tile);
+  load_base(tile, base[0]);
   for (int turn = 0; tile < last; ++tile, turn ^= 1) {
-    Tile now = next;
-    const int l = now.l;
     // the first adapters' B before anything that waits
     unsigned long long left = __ballot(l >= 0) & 0xFFFFull;
     const bool any = left != 0;
@@ -441,9 +437,9 @@ __global__ __launch_bounds__(kUpWaves * 64) void kq_adapter_up_kernel(const Adap
 #pragma unroll
     for (int k = 0; k < D; ++k) a[k] = next_adapter(left, l);
     if (any) load_b(a);
-    if constexpr (!OPERANDS) sum_parts(tile, s_h[turn]);
-    if (tile + 1 < last) next = load_tile(tile + 1);
+    if (tile + 1 < last) load_base(tile + 1, base[1]);
     if constexpr (!OPERANDS) {
+      sum_parts(tile, s_h[turn]);
       const float sc = l >= 0 && p.scaling ? p.scaling[l] : 1.0f;
       lds_barrier();  // two buffers in turn: one barrier per tile
       float h[RS][8];
@@ -454,7 +450,7 @@ __global__ __launch_bounds__(kUpWaves * 64) void kq_adapter_up_kernel(const Adap
 #pragma unroll
         for (int e = 0; e < 8; ++e) h[s][e] = l >= 0 && 32 * s + 8 * g < p.r ? __fmul_rn(v[e / 4][e % 4], sc) : 0.f;
       }
-      now.ex = two_terms<DT, RS>(h, now.hi, now.lo);
+      ex = two_terms<DT, RS>(h, hi, lo);
     }
     f32x4 d[NB];
 #pragma unroll
@@ -470,8 +466,8 @@ __global__ __launch_bounds__(kUpWaves * 64) void kq_adapter_up_kernel(const Adap
           for (int s = 0; s < RS; ++s) {
             u32x4_t b = bv[k][j][s];
             if (ragged) b = 32 * s + 8 * g < p.r ? b : u32x4_t{0, 0, 0, 0};
-            acc = Half<DT>::mma(__builtin_bit_cast(vec, b), now.lo[s], acc);
-            acc = Half<DT>::mma(__builtin_bit_cast(vec, b), now.hi[s], acc);
+            acc = Half<DT>::mma(__builtin_bit_cast(vec, b), lo[s], acc);
+            acc = Half<DT>::mma(__builtin_bit_cast(vec, b), hi[s], acc);
           }
           if (l == a[k]) d[j] = acc;
         }
@@ -481,26 +477,30 @@ __global__ __launch_bounds__(kUpWaves * 64) void kq_adapter_up_kernel(const Adap
       for (int k = 0; k < D; ++k) a[k] = next_adapter(left, l);
       load_b(a);
     }
+    // a row's adapter for the lanes that write it; then the next tile's h into the registers
+    int lt[kPasses];
+#pragma unroll
+    for (int w = 0; w < kPasses; ++w) lt[w] = __shfl(l, tr + 64 / kLanes * w, 64);
     // lane: columns 16 j + 4 g + 0..3 of token lr; the wave's own rows, in its program order
 #pragma unroll
     for (int j = 0; j < NB; ++j) {
       if constexpr (DT == 1)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) d[j][e] = __builtin_ldexpf(d[j][e], -now.ex);
+        for (int e = 0; e < 4; ++e) d[j][e] = __builtin_ldexpf(d[j][e], -ex);
       *reinterpret_cast<f32x4 *>(mine + lr * kRow + 16 * j + 4 * g) = d[j];
     }
+    if (tile + 1 < last) load_h(tile + 1);
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
 #pragma unroll
     for (int w = 0; w < kPasses; ++w) {
       const int row = tr + 64 / kLanes * w;
       const int64_t t = tile * 16 + row;
-      const int lt = __shfl(l, row, 64);
-      u32x4_t o = now.base[w];
-      if (lt >= 0) {
+      u32x4_t o = base[0][w];
+      if (lt[w] >= 0) {
         const f32x4 *q = reinterpret_cast<const f32x4 *>(mine + row * kRow + 8 * (lane % kLanes));
         const f32x4 add[2] = {q[0], q[1]};
-        const one *b = reinterpret_cast<const one *>(&now.base[w]);
+        const one *b = reinterpret_cast<const one *>(&base[0][w]);
         one v[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] = Half<DT>::round(__fadd_rn((float)b[e], add[e / 4][e % 4]));
@@ -511,6 +511,7 @@ __global__ __launch_bounds__(kUpWaves * 64) void kq_adapter_up_kernel(const Adap
         if constexpr (OPERANDS) __builtin_nontemporal_store(o, to);
         else *to = o;
       }
+      base[0][w] = base[1][w];
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
@@ -544,7 +545,8 @@ template <int DT, int RS, int NB, int D, bool OPERANDS>
 hipError_t launch_up(AdapterArgs a, hipStream_t s) {
   constexpr int kCols = 16 * NB * kUpWaves;
   const int64_t t16 = (a.T + 15) / 16, cols = (a.N + kCols - 1) / kCols;
-  // some 4096 workgroups, each over a run of tiles whose adapter's B it keeps
+  // some 4096 workgroups, each over a run of tiles whose adapter's B it keeps (8192 tokens, N
+  // 14336, r 64: 151 us for both kernels; one round of 1024 workgroups 170, 8192 workgroups 164)
   int64_t run = t16 * cols / 4096;
   if (run < 1) run = 1;
   if (run > 64) run = 64;
