@@ -354,7 +354,8 @@ kq_status kq_rmsnorm_quant(const void *x, int64_t ldx, const void *residual, int
  * E is 1 .. 4096. R == 0 or N == 0 returns KQ_OK and launches nothing. The call does not read
  * offsets or rows on the host, so their values may change between replays of a captured
  * graph. Asynchronous on `stream`; no allocation. Errors: INVALID_ARG (NULLs, sizes, strides
- * too small, bits, dtypes), UNSUPPORTED (K, E or the grid not as above), ALIGNMENT, HIP.
+ * too small, bits, dtypes), UNSUPPORTED (K or E not as above, a row stride of wq of 16 MiB or
+ * more, sizes or strides of 2^31 or more), ALIGNMENT, HIP.
  */
 kq_status kq_grouped_gemm(const uint8_t *xq, int64_t ldxq, const void *sx, int64_t T,
                           const int32_t *rows, int64_t R, const uint8_t *wq, int64_t ldwq,
@@ -386,7 +387,8 @@ kq_status kq_grouped_gemm(const uint8_t *xq, int64_t ldxq, const void *sx, int64
  * T == 0 or N == 0 returns KQ_OK and launches nothing. Asynchronous on `stream`; no
  * allocation; the result does not depend on the order of the sums' parts (no atomics).
  * Errors: INVALID_ARG (NULLs, sizes, strides too small, dtype, overlaps), UNSUPPORTED
- * (K, N or r not as above), ALIGNMENT, WORKSPACE, HIP.
+ * (K, N or r not as above, T above 2^27, ldx above 2^25, other strides of 2^31 or more),
+ * ALIGNMENT, WORKSPACE, HIP.
  */
 kq_status kq_adapter_workspace_size(int64_t T, int64_t K, int64_t r, size_t *bytes);
 kq_status kq_adapter_add(const void *x, int64_t ldx, const void *A, const void *B,

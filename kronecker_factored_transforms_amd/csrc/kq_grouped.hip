@@ -222,13 +222,8 @@ __global__ __launch_bounds__(WAVES * 64) void kq_grouped_stream_kernel(const Gro
     }
 }
 
-// ---- the tile kernel: 256 output channels x up to 256 rows of one group ----
-constexpr int kBM = 256, kBN = 256;
-constexpr int kTileWaves = 8;
-constexpr int kStep = 128;             // bytes of every row per step of the reduction
-constexpr int kOpBytes = kBM * kStep;  // 32 KiB per operand and buffer, two buffers
-constexpr int kLoads = kOpBytes / 1024 / kTileWaves;
-static_assert(kBM == kBN && kLoads * 1024 * kTileWaves == kOpBytes, "one layout for both operands");
+// ---- the tile kernels: 256 output channels x up to 256 rows of one group, or 128 x 128 ----
+constexpr int kStep = 128;  // bytes of every row per step of the reduction
 
 typedef int i32x16 __attribute__((ext_vector_type(16)));
 
@@ -248,31 +243,50 @@ __device__ __forceinline__ i32x4 unpack16(unsigned x, unsigned y) {
   return i32x4{(int)((x << 4) & kHi), (int)(x & kHi), (int)((y << 4) & kHi), (int)(y & kHi)};
 }
 
-// The waves' shares. INT4: 2 x 4 waves of 128 channels x 4 blocks of 16 rows (16x16x64
-// instructions); INT8: 4 x 2 waves of 64 channels x 4 blocks of 32 rows (32x32x32). A wave's
-// blocks stand 64 rows apart, so with NU blocks each the waves cover the first 64 NU rows of
-// the tile and a group's short last tile costs what it holds.
-template <int BITS>
+// The tiles and the waves' shares of them: kMI blocks of kSide channels by kBlocks blocks of kSide
+// rows per wave, INT4 on 16x16x64 instructions, INT8 on 32x32x32. A wave's blocks stand kApart
+// rows apart, so with NU blocks each the waves cover the first NU kApart rows of the tile and a
+// group's short last tile costs what it holds.
+template <int BITS, int SIDE>
 struct Share;
 template <>
-struct Share<4> {
-  static constexpr int kWM = 2, kWN = 4, kSide = 16, kMI = 8;
+struct Share<4, 256> {
+  static constexpr int kWM = 2, kWN = 4, kSide = 16;
   typedef i32x4 acc_t;
 };
 template <>
-struct Share<8> {
-  static constexpr int kWM = 4, kWN = 2, kSide = 32, kMI = 2;
+struct Share<8, 256> {
+  static constexpr int kWM = 4, kWN = 2, kSide = 32;
   typedef i32x16 acc_t;
 };
+template <>
+struct Share<4, 128> {
+  static constexpr int kWM = 2, kWN = 2, kSide = 16;
+  typedef i32x4 acc_t;
+};
+template <>
+struct Share<8, 128> {
+  static constexpr int kWM = 2, kWN = 2, kSide = 32;
+  typedef i32x16 acc_t;
+};
+template <int BITS, int SIDE>
+struct Tiling : Share<BITS, SIDE> {
+  typedef Share<BITS, SIDE> S;
+  static constexpr int kWaves = S::kWM * S::kWN;
+  static constexpr int kMI = SIDE / S::kWM / S::kSide, kApart = S::kWN * S::kSide, kBlocks = SIDE / kApart;
+  static constexpr int kOpBytes = SIDE * kStep;  // per operand and buffer, two buffers
+  static constexpr int kLoads = kOpBytes / 1024 / kWaves;
+  static_assert(kLoads * 1024 * kWaves == kOpBytes, "the tile splits evenly over the waves");
+};
 
-template <int BITS, int OUT, int NU>
+template <int BITS, int SIDE, int OUT, int NU>
 __device__ __forceinline__ void tile_product(const GroupedArgs &p, const RowTile &tile, int64_t n0,
                                              unsigned char *s_buf) {
-  typedef Share<BITS> S;
+  typedef Tiling<BITS, SIDE> S;
   typedef typename S::acc_t acc_t;
+  constexpr int kOpBytes = S::kOpBytes, kLoads = S::kLoads;
   constexpr int kRegs = sizeof(acc_t) / 4;
   constexpr int kChunks = kStep / 16, kRowsPer = 1024 / kStep;
-  static_assert(S::kWN * S::kSide == 64 && S::kWM * S::kWN == kTileWaves, "blocks of a wave: 64 rows apart");
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int g = lane / S::kSide, lr = lane % S::kSide;
@@ -299,18 +313,18 @@ __device__ __forceinline__ void tile_product(const GroupedArgs &p, const RowTile
     ax[j] = p.xq + t * p.ldxq + piece * 16;
   }
   const int steps = (p.pieces + kChunks - 1) / kChunks;
-  auto dma_step = [&](int ks, int b, int j0 = 0, int j1 = kLoads) {
+  auto dma_step = [&](int ks, int b) {
     if ((ks + 1) * kChunks <= p.pieces) {
       const uint8_t *w = wbase + (int64_t)ks * kStep;
 #pragma unroll
-      for (int j = j0; j < j1; ++j) {
+      for (int j = 0; j < kLoads; ++j) {
         dma16<false>(w, vw[j], lds_addr(buf(b) + (wave * kLoads + j) * 1024));
         dma16_addr<false>(ax[j], lds_addr(buf(b) + kOpBytes + (wave * kLoads + j) * 1024));
         ax[j] += kStep;
       }
     } else {  // the last step of a row that ends inside it: the rest comes from a block of zeros
 #pragma unroll
-      for (int j = j0; j < j1; ++j) {
+      for (int j = 0; j < kLoads; ++j) {
         const int R = (wave * kLoads + j) * kRowsPer + lane / kChunks;
         const bool in = ks * kChunks + ((lane % kChunks) ^ swz(R)) < p.pieces;
         dma16_addr<false>(in ? wbase + (int64_t)ks * kStep + vw[j] : kZeros,
@@ -330,14 +344,14 @@ __device__ __forceinline__ void tile_product(const GroupedArgs &p, const RowTile
 
   // rows of this lane's fragments: swz is swz(lr) for all of them
   const int sl = swz(lr);
-  const int row_w = wm * (kBM / S::kWM) + lr, row_x = wn * S::kSide + lr;
+  const int row_w = wm * (SIDE / S::kWM) + lr, row_x = wn * S::kSide + lr;
   // The steps of this lane's rows, and which of them are written: loaded here, so that the
   // epilogue does not wait for them (a row's number, then its step) row by row.
   float sx[NU];
   int written = 0;
 #pragma unroll
   for (int i = 0; i < NU; ++i) {
-    const int R = row_x + i * 64;
+    const int R = row_x + i * S::kApart;
     int64_t t = tile.begin + (R < tile.count ? R : 0);
     if (p.rows) t = p.rows[t];
     const bool in = t >= 0 && t < p.T;
@@ -359,7 +373,7 @@ __device__ __forceinline__ void tile_product(const GroupedArgs &p, const RowTile
       f.w[m] = *reinterpret_cast<const u32x4_t *>(w + (row_w + m * S::kSide) * kStep + off);
 #pragma unroll
     for (int i = 0; i < NU; ++i)
-      f.x[i] = *reinterpret_cast<const u32x4_t *>(w + kOpBytes + (row_x + i * 64) * kStep + off);
+      f.x[i] = *reinterpret_cast<const u32x4_t *>(w + kOpBytes + (row_x + i * S::kApart) * kStep + off);
     return f;
   };
   auto multiply = [&](const Part &f) {
@@ -443,14 +457,14 @@ __device__ __forceinline__ void tile_product(const GroupedArgs &p, const RowTile
   // consecutive channels. (Staging the rows in LDS for whole-line stores was slower: 1055 us
   // against 1018 on 16384 x 14336 x 4096 INT8, its barriers cost more than the stores gained.)
   constexpr int kQ = S::kMI * kRegs / 4;  // groups of 4 channels
-  const int64_t nl = n0 + wm * (kBM / S::kWM) + 4 * g;  // group q: nl + group_at(q)
+  const int64_t nl = n0 + wm * (SIDE / S::kWM) + 4 * g;  // group q: nl + group_at(q)
   auto group_at = [](int q) { return q / (kRegs / 4) * S::kSide + q % (kRegs / 4) * 4 * (64 / S::kSide); };
   float sw[kQ][4];
   load_steps<kQ>(p.sw, tile.e * p.N, nl, p.N, p.scale_fp16, group_at, sw);
 #pragma unroll
   for (int i = 0; i < NU; ++i) {
     if (!(written >> i & 1)) continue;
-    const int64_t row = (tile.begin + row_x + i * 64) * p.ldo + nl;
+    const int64_t row = (tile.begin + row_x + i * S::kApart) * p.ldo + nl;
 #pragma unroll
     for (int q = 0; q < kQ; ++q) {
       float v[4];
@@ -464,16 +478,23 @@ __device__ __forceinline__ void tile_product(const GroupedArgs &p, const RowTile
   }
 }
 
-template <int BITS, int OUT>
-__global__ __launch_bounds__(kTileWaves * 64) void kq_grouped_tile_kernel(const GroupedArgs p, int tiles_m) {
-  __shared__ __align__(16) unsigned char s_buf[4 * kOpBytes];
-  const RowTile tile = find_tile<kBN>(p.offsets, p.E, p.R, (int)(blockIdx.x / tiles_m));
+template <int BITS, int SIDE, int OUT>
+__global__ __launch_bounds__((Tiling<BITS, SIDE>::kWaves * 64)) void kq_grouped_tile_kernel(const GroupedArgs p, int tiles_m) {
+  typedef Tiling<BITS, SIDE> S;
+  __shared__ __align__(16) unsigned char s_buf[4 * S::kOpBytes];
+  const RowTile tile = find_tile<SIDE>(p.offsets, p.E, p.R, (int)(blockIdx.x / tiles_m));
   if (tile.e < 0) return;
-  const int64_t n0 = (int64_t)(blockIdx.x % tiles_m) * kBM;
-  if (tile.count > 192) tile_product<BITS, OUT, 4>(p, tile, n0, s_buf);
-  else if (tile.count > 128) tile_product<BITS, OUT, 3>(p, tile, n0, s_buf);
-  else if (tile.count > 64) tile_product<BITS, OUT, 2>(p, tile, n0, s_buf);
-  else tile_product<BITS, OUT, 1>(p, tile, n0, s_buf);
+  const int64_t n0 = (int64_t)(blockIdx.x % tiles_m) * SIDE;
+  if constexpr (S::kBlocks == 4) {
+    if (tile.count > 3 * S::kApart) tile_product<BITS, SIDE, OUT, 4>(p, tile, n0, s_buf);
+    else if (tile.count > 2 * S::kApart) tile_product<BITS, SIDE, OUT, 3>(p, tile, n0, s_buf);
+    else if (tile.count > S::kApart) tile_product<BITS, SIDE, OUT, 2>(p, tile, n0, s_buf);
+    else tile_product<BITS, SIDE, OUT, 1>(p, tile, n0, s_buf);
+  } else {
+    static_assert(S::kBlocks == 2, "blocks of a wave");
+    if (tile.count > S::kApart) tile_product<BITS, SIDE, OUT, 2>(p, tile, n0, s_buf);
+    else tile_product<BITS, SIDE, OUT, 1>(p, tile, n0, s_buf);
+  }
 }
 
 template <int BITS>
@@ -487,28 +508,43 @@ kq_status launch_stream(const GroupedArgs &a, hipStream_t s) {
   return hipGetLastError() == hipSuccess ? KQ_OK : KQ_ERR_HIP;
 }
 
-template <int BITS>
+template <int BITS, int SIDE>
 kq_status launch_tile(const GroupedArgs &a, hipStream_t s) {
-  const int64_t tiles_m = (a.N + kBM - 1) / kBM;
-  const int64_t tiles = a.R / kBN + (a.R < a.E ? a.R : a.E);
-  if (tiles_m * tiles > 0x7FFFFFFF / (kTileWaves * 64)) return KQ_ERR_UNSUPPORTED;
-  const dim3 grid((unsigned)(tiles_m * tiles)), block(kTileWaves * 64);
+  constexpr int kThreads = Tiling<BITS, SIDE>::kWaves * 64;
+  const int64_t tiles_m = (a.N + SIDE - 1) / SIDE;
+  const int64_t tiles = a.R / SIDE + (a.R < a.E ? a.R : a.E);
+  if (tiles_m * tiles > 0x7FFFFFFF / kThreads) return KQ_ERR_UNSUPPORTED;
+  const dim3 grid((unsigned)(tiles_m * tiles)), block(kThreads);
   if (a.out_dtype == KQ_FP32)
-    hipLaunchKernelGGL((kq_grouped_tile_kernel<BITS, KQ_FP32>), grid, block, 0, s, a, (int)tiles_m);
+    hipLaunchKernelGGL((kq_grouped_tile_kernel<BITS, SIDE, KQ_FP32>), grid, block, 0, s, a, (int)tiles_m);
   else if (a.out_dtype == KQ_BF16)
-    hipLaunchKernelGGL((kq_grouped_tile_kernel<BITS, KQ_BF16>), grid, block, 0, s, a, (int)tiles_m);
+    hipLaunchKernelGGL((kq_grouped_tile_kernel<BITS, SIDE, KQ_BF16>), grid, block, 0, s, a, (int)tiles_m);
   else
-    hipLaunchKernelGGL((kq_grouped_tile_kernel<BITS, KQ_FP16>), grid, block, 0, s, a, (int)tiles_m);
+    hipLaunchKernelGGL((kq_grouped_tile_kernel<BITS, SIDE, KQ_FP16>), grid, block, 0, s, a, (int)tiles_m);
   return hipGetLastError() == hipSuccess ? KQ_OK : KQ_ERR_HIP;
 }
 
-// Few rows per group: the weights' stream bounds the product; more: the matrix cores do.
-#ifndef GROUPED_CUT
-#define GROUPED_CUT 32
-#endif
+// Which kernel, by the rows per group and the workgroups that each tile size would make (us; R
+// rows, E groups):
+//   the stream kernel, where 128 x 128 tiles are too few to keep the card's loads going and the
+//   rows too few to ask for more than loads, or where such tiles are very few:
+//     R 8, E 8, N 4096, K 4096 INT8 (256 tiles of 128): 16.7 against 24.6; R 64: 25.4, 32.5;
+//     R 2040, E 2, N 88, K 8576 INT4 (17 tiles): 21 against 45;
+//     but R 256, E 32, N 2048, K 7168 INT8 (544 tiles): 104 against 82; R 300, E 2, N 4096,
+//     K 4096 INT8 (128 tiles, 150 rows a group): 43 against 34;
+//   256 x 256 tiles, where the groups fill them and there are enough for the 256 compute units:
+//     R 16384, E 8, N 14336, K 4096: INT4 858 against 911, INT8 1054 against 1254;
+//     but R 8192, E 4, N 512, K 8192 INT8 (72 tiles of 256): 110 against 73; R 2048, E 64,
+//     N 4096, K 7168 INT4 (32 rows a group): 222 against 182;
+//   128 x 128 tiles otherwise (two workgroups of them share a compute unit).
 template <int BITS>
 kq_status launch(const GroupedArgs &a, hipStream_t s) {
-  return a.R >= GROUPED_CUT * (int64_t)a.E ? launch_tile<BITS>(a, s) : launch_stream<BITS>(a, s);
+  const int64_t groups = a.R < a.E ? a.R : a.E, per_group = a.R / groups;
+  const int64_t tiles128 = (a.N + 127) / 128 * (a.R / 128 + groups);
+  const int64_t tiles256 = (a.N + 255) / 256 * (a.R / 256 + groups);
+  if (tiles128 < 64 || (tiles128 < 512 && per_group <= 16)) return launch_stream<BITS>(a, s);
+  if (per_group >= 96 && tiles256 >= 192) return launch_tile<BITS, 256>(a, s);
+  return launch_tile<BITS, 128>(a, s);
 }
 
 constexpr int64_t kMax31 = 0x7FFFFFFF;
