@@ -100,6 +100,32 @@ __device__ __forceinline__ void store_out4(void *out, int64_t i, const float (&v
   }
 }
 
+// 16 bytes of finished outputs, of which the first `left` values exist, to out[i]
+template <int OUT>
+__device__ __forceinline__ void store_piece(void *out, int64_t i, const u32x4_t &v, int64_t left) {
+  if constexpr (OUT == KQ_FP32) {
+    typedef u32x4_t any __attribute__((aligned(4)));
+    float *o = reinterpret_cast<float *>(out) + i;
+    if (left >= 4) {
+      *reinterpret_cast<any *>(o) = v;
+    } else {
+#pragma unroll
+      for (int r = 0; r < 3; ++r)
+        if (r < left) o[r] = __uint_as_float(v[r]);
+    }
+  } else {
+    typedef u32x4_t any __attribute__((aligned(2)));
+    uint16_t *o = reinterpret_cast<uint16_t *>(out) + i;
+    if (left >= 8) {
+      *reinterpret_cast<any *>(o) = v;
+    } else {
+#pragma unroll
+      for (int r = 0; r < 7; ++r)
+        if (r < left) o[r] = (uint16_t)(v[r / 2] >> (16 * (r % 2)));
+    }
+  }
+}
+
 // Steps of Q groups of 4 channels, group q from channel n + at(q) on, of a row of N steps that
 // starts at `row`; channels past N get 0 (their outputs are not written).
 template <int Q, typename At>
@@ -275,13 +301,15 @@ struct Tiling : Share<BITS, SIDE> {
   static constexpr int kWaves = S::kWM * S::kWN;
   static constexpr int kMI = SIDE / S::kWM / S::kSide, kApart = S::kWN * S::kSide, kBlocks = SIDE / kApart;
   static constexpr int kOpBytes = SIDE * kStep;  // per operand and buffer, two buffers
+  static constexpr int kOutBytes = 2 * kApart * (SIDE * 4 + 16);  // two blocks of fp32 output rows
+  static constexpr int kLds = 4 * kOpBytes > kOutBytes ? 4 * kOpBytes : kOutBytes;
   static constexpr int kLoads = kOpBytes / 1024 / kWaves;
   static_assert(kLoads * 1024 * kWaves == kOpBytes, "the tile splits evenly over the waves");
 };
 
 template <int BITS, int SIDE, int OUT, int NU>
 __device__ __forceinline__ void tile_product(const GroupedArgs &p, const RowTile &tile, int64_t n0,
-                                             unsigned char *s_buf) {
+                                             unsigned char *s_buf, unsigned char *s_ok) {
   typedef Tiling<BITS, SIDE> S;
   typedef typename S::acc_t acc_t;
   constexpr int kOpBytes = S::kOpBytes, kLoads = S::kLoads;
@@ -348,7 +376,6 @@ __device__ __forceinline__ void tile_product(const GroupedArgs &p, const RowTile
   // The steps of this lane's rows, and which of them are written: loaded here, so that the
   // epilogue does not wait for them (a row's number, then its step) row by row.
   float sx[NU];
-  int written = 0;
 #pragma unroll
   for (int i = 0; i < NU; ++i) {
     const int R = row_x + i * S::kApart;
@@ -356,7 +383,7 @@ __device__ __forceinline__ void tile_product(const GroupedArgs &p, const RowTile
     if (p.rows) t = p.rows[t];
     const bool in = t >= 0 && t < p.T;
     sx[i] = load_step(p.sx, in ? t : 0, p.scale_fp16);
-    if (R < tile.count && in) written |= 1 << i;
+    if (wm == 0 && g == 0) s_ok[R] = R < tile.count && in;  // read behind the reduction's barriers
   }
 
   // A step's fragments come in kParts parts, each read while the part before it multiplies;
@@ -453,18 +480,24 @@ __device__ __forceinline__ void tile_product(const GroupedArgs &p, const RowTile
     }
   }
 
-  // Epilogue: a lane holds row wn * side + lr of each block and, per group of 4 registers, 4
-  // consecutive channels. (Staging the rows in LDS for whole-line stores was slower: 1055 us
-  // against 1018 on 16384 x 14336 x 4096 INT8, its barriers cost more than the stores gained.)
+  // Epilogue, kApart rows at a time (block i of every wave): a lane holds one row's 4 consecutive
+  // channels per group of 4 registers, 8 bytes of 16 or 32 different lines an instruction. Through
+  // LDS a wave stores whole rows of the tile, 16 bytes a lane. Two places in turn, one barrier per
+  // block.
   constexpr int kQ = S::kMI * kRegs / 4;  // groups of 4 channels
-  const int64_t nl = n0 + wm * (SIDE / S::kWM) + 4 * g;  // group q: nl + group_at(q)
+  constexpr int kSize = OUT == KQ_FP32 ? 4 : 2, kRowBytes = SIDE * kSize + 16;
+  constexpr int kRowLanes = SIDE * kSize / 16, kAtOnce = 64 / kRowLanes, kPer = 16 / kSize;
+  static_assert(2 * S::kApart * kRowBytes <= S::kLds, "two places of rows");
+  const int ml = wm * (SIDE / S::kWM) + 4 * g;  // this lane's channels: ml + group_at(q)
   auto group_at = [](int q) { return q / (kRegs / 4) * S::kSide + q % (kRegs / 4) * 4 * (64 / S::kSide); };
   float sw[kQ][4];
-  load_steps<kQ>(p.sw, tile.e * p.N, nl, p.N, p.scale_fp16, group_at, sw);
+  load_steps<kQ>(p.sw, tile.e * p.N, n0 + ml, p.N, p.scale_fp16, group_at, sw);
+  const int64_t nc = n0 + lane % kRowLanes * kPer;  // the channels this lane stores
+  wait_and_fence<kWaitLgkm0>();
+  sync();  // every wave has read the last step
 #pragma unroll
   for (int i = 0; i < NU; ++i) {
-    if (!(written >> i & 1)) continue;
-    const int64_t row = (tile.begin + row_x + i * S::kApart) * p.ldo + nl;
+    unsigned char *rows = s_buf + (i & 1) * (S::kApart * kRowBytes);
 #pragma unroll
     for (int q = 0; q < kQ; ++q) {
       float v[4];
@@ -473,7 +506,18 @@ __device__ __forceinline__ void tile_product(const GroupedArgs &p, const RowTile
         const int a = acc[q / (kRegs / 4)][i][q % (kRegs / 4) * 4 + r];
         v[r] = __fmul_rn(__fmul_rn((float)(BITS == 8 ? a : a >> 8), sx[i]), sw[q][r]);
       }
-      store_out4<OUT>(p.out, row + group_at(q), v, p.N - nl - group_at(q));
+      store_out4<OUT>(rows + row_x * kRowBytes, ml + group_at(q), v, 4);
+    }
+    const unsigned long long ok = __ballot(lane < S::kApart && s_ok[i * S::kApart + lane % S::kApart]);
+    wait_and_fence<kWaitLgkm0>();
+    sync();
+#pragma unroll
+    for (int k = 0; k < S::kApart / (kAtOnce * S::kWaves); ++k) {
+      const int r = (k * S::kWaves + wave) * kAtOnce + lane / kRowLanes;
+      if (ok >> r & 1)
+        store_piece<OUT>(p.out, (tile.begin + i * S::kApart + r) * p.ldo + nc,
+                         *reinterpret_cast<const u32x4_t *>(rows + r * kRowBytes + lane % kRowLanes * 16),
+                         p.N - nc);
     }
   }
 }
@@ -481,19 +525,20 @@ __device__ __forceinline__ void tile_product(const GroupedArgs &p, const RowTile
 template <int BITS, int SIDE, int OUT>
 __global__ __launch_bounds__((Tiling<BITS, SIDE>::kWaves * 64)) void kq_grouped_tile_kernel(const GroupedArgs p, int tiles_m) {
   typedef Tiling<BITS, SIDE> S;
-  __shared__ __align__(16) unsigned char s_buf[4 * S::kOpBytes];
+  __shared__ __align__(16) unsigned char s_buf[S::kLds];
+  __shared__ unsigned char s_ok[SIDE];  // which rows of the tile are written
   const RowTile tile = find_tile<SIDE>(p.offsets, p.E, p.R, (int)(blockIdx.x / tiles_m));
   if (tile.e < 0) return;
   const int64_t n0 = (int64_t)(blockIdx.x % tiles_m) * SIDE;
   if constexpr (S::kBlocks == 4) {
-    if (tile.count > 3 * S::kApart) tile_product<BITS, SIDE, OUT, 4>(p, tile, n0, s_buf);
-    else if (tile.count > 2 * S::kApart) tile_product<BITS, SIDE, OUT, 3>(p, tile, n0, s_buf);
-    else if (tile.count > S::kApart) tile_product<BITS, SIDE, OUT, 2>(p, tile, n0, s_buf);
-    else tile_product<BITS, SIDE, OUT, 1>(p, tile, n0, s_buf);
+    if (tile.count > 3 * S::kApart) tile_product<BITS, SIDE, OUT, 4>(p, tile, n0, s_buf, s_ok);
+    else if (tile.count > 2 * S::kApart) tile_product<BITS, SIDE, OUT, 3>(p, tile, n0, s_buf, s_ok);
+    else if (tile.count > S::kApart) tile_product<BITS, SIDE, OUT, 2>(p, tile, n0, s_buf, s_ok);
+    else tile_product<BITS, SIDE, OUT, 1>(p, tile, n0, s_buf, s_ok);
   } else {
     static_assert(S::kBlocks == 2, "blocks of a wave");
-    if (tile.count > S::kApart) tile_product<BITS, SIDE, OUT, 2>(p, tile, n0, s_buf);
-    else tile_product<BITS, SIDE, OUT, 1>(p, tile, n0, s_buf);
+    if (tile.count > S::kApart) tile_product<BITS, SIDE, OUT, 2>(p, tile, n0, s_buf, s_ok);
+    else tile_product<BITS, SIDE, OUT, 1>(p, tile, n0, s_buf, s_ok);
   }
 }
 
