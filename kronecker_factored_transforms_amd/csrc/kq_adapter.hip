@@ -2,7 +2,7 @@
 //
 //   out[t] = cvt( base[t] + scaling[l] * B[l] (A[l] x[t]) ),   l = adapter[t].
 //
-// Two kernels. The first forms the low-rank vectors h[t] = A[l] x[t] (K long, r short) and
+// Two kernels (three for 1024 to 4095 tokens). The first forms the low-rank vectors h[t] = A[l] x[t] (K long, r short) and
 // splits K over workgroups where tokens are few; each part goes to the workspace as fp32. The
 // second adds the parts up in their order (no atomics: the result does not depend on which
 // workgroup ends first), scales, and forms B[l] h + base.
@@ -48,17 +48,22 @@ struct AdapterArgs {
   const int32_t *adapter;
   const float *scaling;
   void *out;
-  void *ws;  // h: parts or operands (see Workspace)
+  float *part;  // h's parts, and h as operands: what lies between the kernels, see below
+  void *ops;
   int64_t ldx, ldb, ldo, T;
   int K, N, r, L, splits, split_steps;  // a step: kStep values of K
   int tiles_per_group;                  // up: token tiles of one workgroup
 };
 
-// What lies between the two kernels. Few tokens: the parts of h over K, fp32,
-// [splits][T][ranks up to a multiple of 16]. Many (one part): h as the second product's
-// operands, [tile of 16 tokens][steps of 32 ranks][first, second term][lane][8 values], and the
-// exponent of the power of two each token's h was multiplied by, [tile][16].
-constexpr int64_t kWide = 4096;  // from this many tokens on: operands
+// What lies between the kernels. The parts of h over K, fp32, [splits][T][ranks up to a multiple
+// of 16]; and h as the last product's operands, [tile of 16 tokens][steps of 32 ranks][first,
+// second term][lane][8 values], with the exponent of the power of two that each token's h was
+// multiplied by, [tile][16]. Few tokens: parts, which the last kernel adds up itself; from kJoin
+// tokens on: parts, and a kernel in between that makes the operands of them (each would be added
+// up for every 256 columns otherwise); from kWide on: K is whole, and the first kernel makes them.
+constexpr int64_t kJoin = 1024, kWide = 4096;
+
+constexpr int kParts = 8;  // of K, at most
 
 __device__ __forceinline__ int round16(int r) { return (r + 15) / 16 * 16; }
 
@@ -106,6 +111,21 @@ __device__ __forceinline__ int two_terms(const float (&h)[RS][8], typename Half<
       lo[s][e] = Half<DT>::round(__builtin_isfinite((float)a) ? __fsub_rn(v, (float)a) : 0.f);
     }
   return ex;
+}
+
+// A tile's operands: the terms of two_terms() as the lanes hold them, and the exponents
+template <int DT, int RS>
+__device__ __forceinline__ void store_operands(const AdapterArgs &p, int64_t tile, int64_t tiles,
+                                               const typename Half<DT>::vec (&hi)[RS],
+                                               const typename Half<DT>::vec (&lo)[RS], int ex) {
+  const int lane = threadIdx.x & 63;
+  auto *o = reinterpret_cast<typename Half<DT>::vec *>(p.ops);
+#pragma unroll
+  for (int s = 0; s < RS; ++s) {
+    o[tile * (RS * 2 * 64) + (2 * s) * 64 + lane] = hi[s];
+    o[tile * (RS * 2 * 64) + (2 * s + 1) * 64 + lane] = lo[s];
+  }
+  if (lane < 16) reinterpret_cast<int *>(o + tiles * (RS * 2 * 64))[tile * 16 + lane] = ex;
 }
 
 constexpr int kStep = 64;  // values of K per step: rows of 128 bytes in LDS
@@ -261,7 +281,7 @@ __global__ __launch_bounds__(WAVES * 64) void kq_adapter_down_kernel(const Adapt
         if constexpr (OPERANDS)
           kept[i / WAVES] = v;
         else if (16 * b < round16(p.r))
-          *reinterpret_cast<f32x4 *>(reinterpret_cast<float *>(p.ws) +
+          *reinterpret_cast<f32x4 *>(p.part +
                                      ((int64_t)blockIdx.y * p.T + t0 + 16 * f + lr) * round16(p.r) + 16 * b +
                                      4 * g) = v;
       }
@@ -318,18 +338,43 @@ __global__ __launch_bounds__(WAVES * 64) void kq_adapter_down_kernel(const Adapt
       typename Half<DT>::vec hi[RS], lo[RS];
       const int ex = two_terms<DT, RS>(h, hi, lo);
       const int64_t tile = t0 / 16 + f, tiles = (p.T + 15) / 16;
-      if (tile < tiles) {
-        auto *o = reinterpret_cast<typename Half<DT>::vec *>(p.ws) + tile * (RS * 2 * 64) + lane;
-#pragma unroll
-        for (int s = 0; s < RS; ++s) {
-          o[(2 * s) * 64] = hi[s];
-          o[(2 * s + 1) * 64] = lo[s];
-        }
-        if (lane < 16)
-          (reinterpret_cast<int *>(reinterpret_cast<typename Half<DT>::vec *>(p.ws) + tiles * (RS * 2 * 64)))[tile * 16 + lane] = ex;
-      }
+      if (tile < tiles) store_operands<DT, RS>(p, tile, tiles, hi, lo, ex);
     }
   }
+}
+
+// The operands of one tile of 16 tokens, from the parts of its h: one wave
+template <int DT, int RS>
+__global__ __launch_bounds__(64) void kq_adapter_join_kernel(const AdapterArgs p) {
+  const int lane = threadIdx.x & 63, g = lane >> 4, lr = lane & 15;
+  const int64_t tile = blockIdx.x, t = tile * 16 + lr, tc = t < p.T ? t : p.T - 1;
+  const int l = token_adapter(p, t), r16 = round16(p.r);
+  const float sc = l >= 0 && p.scaling ? p.scaling[l] : 1.0f;
+  const float *q = p.part + tc * r16;
+  float h[RS][8];
+#pragma unroll
+  for (int s = 0; s < RS; ++s) {
+    const int k = 32 * s + 8 * g;
+    const bool in = k < p.r;
+    f32x4 w[kParts][2];
+#pragma unroll
+    for (int i = 0; i < kParts; ++i)
+      if (i < p.splits)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          w[i][e] = *reinterpret_cast<const f32x4 *>(q + i * (p.T * r16) + (in ? k : 0) + 4 * e);
+#pragma unroll
+    for (int i = 1; i < kParts; ++i)
+      if (i < p.splits)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) w[0][e] += w[i][e];
+    // what a token without an adapter has there is not written, and dropped
+#pragma unroll
+    for (int e = 0; e < 8; ++e) h[s][e] = l >= 0 && in ? __fmul_rn(w[0][e / 4][e % 4], sc) : 0.f;
+  }
+  typename Half<DT>::vec hi[RS], lo[RS];
+  const int ex = two_terms<DT, RS>(h, hi, lo);
+  store_operands<DT, RS>(p, tile, (p.T + 15) / 16, hi, lo, ex);
 }
 
 constexpr int kUpWaves = 4;
@@ -383,32 +428,32 @@ __global__ __launch_bounds__(kUpWaves * 64) void kq_adapter_up_kernel(const Adap
   auto load_h = [&](int64_t tile) {
     l = token_adapter(p, tile * 16 + lr);
     if constexpr (OPERANDS) {
-      const vec *o = reinterpret_cast<const vec *>(p.ws) + tile * (RS * 2 * 64) + lane;
+      const vec *o = reinterpret_cast<const vec *>(p.ops) + tile * (RS * 2 * 64) + lane;
 #pragma unroll
       for (int s = 0; s < RS; ++s) {
         hi[s] = o[(2 * s) * 64];
         lo[s] = o[(2 * s + 1) * 64];
       }
       if constexpr (DT == 1)
-        ex = (reinterpret_cast<const int *>(reinterpret_cast<const vec *>(p.ws) + tiles * (RS * 2 * 64)))[tile * 16 + lr];
+        ex = (reinterpret_cast<const int *>(reinterpret_cast<const vec *>(p.ops) + tiles * (RS * 2 * 64)))[tile * 16 + lr];
     }
   };
   // The parts' sums, by the whole workgroup: 16 tokens of r16 ranks stand one behind another in
   // each part. What a token without an adapter has there is dropped.
   auto sum_parts = [&](int64_t tile, float *to) {
-    const int r16 = round16(p.r), values = (int)min((int64_t)16, p.T - tile * 16) * r16;
-    const float *q = reinterpret_cast<const float *>(p.ws) + tile * 16 * r16;
-    const int64_t part = p.T * r16;
-    for (int i = threadIdx.x; i < values; i += kUpWaves * 64) {
-      float h = 0.f;
-      int k = 0;
-      for (; k + 4 <= p.splits; k += 4) {
-        const float a = q[k * part + i], b = q[(k + 1) * part + i], c = q[(k + 2) * part + i], d = q[(k + 3) * part + i];
-        h = ((h + a) + b) + c;
-        h += d;
-      }
-      for (; k < p.splits; ++k) h += q[k * part + i];
-      to[i / r16 * kHRow + i % r16] = h;
+    const int r4 = round16(p.r) / 4, quads = (int)min((int64_t)16, p.T - tile * 16) * r4;
+    const f32x4 *q = reinterpret_cast<const f32x4 *>(p.part) + tile * 16 * r4;
+    const int64_t part = p.T * r4;
+    for (int i = threadIdx.x; i < quads; i += kUpWaves * 64) {
+      f32x4 w[kParts];
+#pragma unroll
+      for (int k = 0; k < kParts; ++k)
+        if (k < p.splits) w[k] = q[k * part + i];
+      f32x4 h = w[0];
+#pragma unroll
+      for (int k = 1; k < kParts; ++k)
+        if (k < p.splits) h += w[k];
+      *reinterpret_cast<f32x4 *>(to + i / r4 * kHRow + i % r4 * 4) = h;
     }
   };
 
@@ -525,7 +570,7 @@ int split_count(int64_t T, int64_t K) {
   const int64_t tiles = (T + 15) / 16, steps = (K + kStep - 1) / kStep;
   int64_t s = 512 / tiles;
   if (s > steps / 4) s = steps / 4;
-  return (int)(s < 1 ? 1 : s > 8 ? 8 : s);
+  return (int)(s < 1 ? 1 : s > kParts ? kParts : s);
 }
 
 // The first kernel's waves and each one's ring of LDS: three steps of a single adapter's rows
@@ -574,9 +619,14 @@ hipError_t launch(AdapterArgs a, hipStream_t s) {
   const unsigned groups = (unsigned)(room < 1 ? 1 : room < most ? room : most);
   hipLaunchKernelGGL((kq_adapter_down_kernel<DT, RB, 1, C::kWaves, C::kD, C::kRing, false>),
                      dim3((unsigned)t16, (unsigned)a.splits, groups), dim3(C::kWaves * 64), 0, s, a);
-  const hipError_t e = hipGetLastError();
+  hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  return launch_up<DT, RS, RS <= 2 ? 4 : 2, RB <= 2 ? 4 : RB <= 8 ? 2 : 1, false>(a, s);
+  constexpr int D = RB <= 2 ? 4 : RB <= 8 ? 2 : 1;
+  if (a.T < kJoin) return launch_up<DT, RS, RS <= 2 ? 4 : 2, D, false>(a, s);
+  hipLaunchKernelGGL((kq_adapter_join_kernel<DT, RS>), dim3((unsigned)t16), dim3(64), 0, s, a);
+  e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  return launch_up<DT, RS, RS <= 2 ? 4 : 2, D, true>(a, s);
 }
 
 template <int DT>
@@ -592,11 +642,14 @@ constexpr int64_t kMax31 = 0x7FFFFFFF;
 
 bool off(const void *p, size_t a) { return ((uintptr_t)p % a) != 0; }
 
+int64_t part_bytes(int64_t T, int64_t K, int64_t r) {
+  return T >= kWide ? 0 : (split_count(T, K) * T * ((r + 15) / 16 * 16) * 4 + 255) / 256 * 256;
+}
+
 int64_t workspace_bytes(int64_t T, int64_t K, int64_t r) {
-  // operands: 32 ranks of two 2-byte terms are the 128 bytes that 32 fp32 ranks take
-  const int64_t rb = r <= 16 ? 1 : r <= 32 ? 2 : r <= 64 ? 4 : r <= 128 ? 8 : 16, t16 = (T + 15) / 16 * 16;
-  const int64_t b = T >= kWide ? t16 * ((rb + 1) / 2 * 128 + 4) : split_count(T, K) * T * ((r + 15) / 16 * 16) * 4;
-  return (b + 255) / 256 * 256;
+  // operands: 32 ranks of two 2-byte terms, and a 4-byte exponent, per token of whole tiles
+  const int64_t steps = r <= 32 ? 1 : r <= 64 ? 2 : r <= 128 ? 4 : 8, t16 = (T + 15) / 16 * 16;
+  return part_bytes(T, K, r) + (T >= kJoin ? (t16 * (steps * 128 + 4) + 255) / 256 * 256 : 0);
 }
 
 kq_status check_sizes(int64_t T, int64_t K, int64_t r) {
@@ -644,8 +697,9 @@ static kq_status adapter_add_impl(const void *x, int64_t ldx, const void *A, con
   if (!workspace || ws_bytes < (size_t)need) return KQ_ERR_WORKSPACE;
   if (off(workspace, 256)) return KQ_ERR_ALIGNMENT;
   const int splits = split_count(T, K), steps = (int)((K + kStep - 1) / kStep);
-  const AdapterArgs a = {x, A, B, base, adapter, scaling, out, workspace, ldx, ldb, ldo, T, (int)K, (int)N,
-                         (int)r, (int)L, splits, (steps + splits - 1) / splits, 1};
+  const AdapterArgs a = {x, A, B, base, adapter, scaling, out, static_cast<float *>(workspace),
+                         static_cast<char *>(workspace) + part_bytes(T, K, r), ldx, ldb, ldo, T, (int)K,
+                         (int)N, (int)r, (int)L, splits, (steps + splits - 1) / splits, 1};
   hipStream_t s = static_cast<hipStream_t>(stream);
   const hipError_t e = dtype == KQ_BF16 ? dispatch<0>(a, s) : dispatch<1>(a, s);
   return e == hipSuccess ? KQ_OK : KQ_ERR_HIP;
