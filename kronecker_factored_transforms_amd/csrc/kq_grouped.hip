@@ -173,7 +173,10 @@ __device__ __forceinline__ void mfma_piece(const u32x4_t &a, const u32x4_t &b, i
 }
 
 // A workgroup: 16 MI output channels x 16 NI rows of one group; its waves split the reduction
-// (64 bytes of a row in turn) and add their parts up in LDS (integers: any order).
+// (64 bytes of a row in turn) and add their parts up in LDS (integers: any order). Bound by the
+// weights' stream: the operands come straight from memory, and as many waves as fit keep their
+// loads going (8 of them a workgroup, one step each: 2 rows of 4096 x 4096 INT8 8.7 us, 4 waves
+// 10.3; 64 rows over 8 experts 26.9, with 4 steps of a wave in flight and fewer waves 30).
 template <int BITS, int MI, int NI, int WAVES>
 __global__ __launch_bounds__(WAVES * 64) void kq_grouped_stream_kernel(const GroupedArgs p, int tiles_m) {
   __shared__ i32x4 s_acc[WAVES][MI * NI][64];
@@ -205,21 +208,19 @@ __global__ __launch_bounds__(WAVES * 64) void kq_grouped_stream_kernel(const Gro
   for (int m = 0; m < MI; ++m)
 #pragma unroll
     for (int j = 0; j < NI; ++j) acc[m][j] = i32x4{0, 0, 0, 0};
-  const int used = (tile.count + 15) / 16;  // 16-row blocks with a row in them
   for (int s = wave; s * 4 < p.pieces; s += WAVES) {
     const bool in = s * 4 + g < p.pieces;  // the last step may have fewer than 4 pieces
+    const int64_t o = in ? (int64_t)s * 64 : -(int64_t)g * 16;
     const u32x4_t zero = {0, 0, 0, 0};
-    u32x4_t a[MI];
+    u32x4_t a[MI], b[NI];
 #pragma unroll
-    for (int m = 0; m < MI; ++m)
-      a[m] = in ? *reinterpret_cast<const u32x4_t *>(wrow[m] + (int64_t)s * 64) : zero;
+    for (int m = 0; m < MI; ++m) a[m] = *reinterpret_cast<const u32x4_t *>(wrow[m] + o);
 #pragma unroll
-    for (int j = 0; j < NI; ++j) {
-      if (j >= used) break;
-      const u32x4_t b = in ? *reinterpret_cast<const u32x4_t *>(xrow[j] + (int64_t)s * 64) : zero;
+    for (int j = 0; j < NI; ++j) b[j] = *reinterpret_cast<const u32x4_t *>(xrow[j] + o);
 #pragma unroll
-      for (int m = 0; m < MI; ++m) mfma_piece<BITS>(a[m], b, acc[m][j]);
-    }
+    for (int j = 0; j < NI; ++j)
+#pragma unroll
+      for (int m = 0; m < MI; ++m) mfma_piece<BITS>(a[m], in ? b[j] : zero, acc[m][j]);
   }
 #pragma unroll
   for (int m = 0; m < MI; ++m)
@@ -542,9 +543,9 @@ __global__ __launch_bounds__((Tiling<BITS, SIDE>::kWaves * 64)) void kq_grouped_
   }
 }
 
-template <int BITS>
+template <int BITS, int NI>
 kq_status launch_stream(const GroupedArgs &a, hipStream_t s) {
-  constexpr int MI = 2, NI = 2, WAVES = 4;
+  constexpr int MI = 2, WAVES = 8;
   const int64_t tiles_m = (a.N + 16 * MI - 1) / (16 * MI);
   const int64_t tiles = a.R / (16 * NI) + (a.R < a.E ? a.R : a.E);
   if (tiles_m * tiles > 0x7FFFFFFF / (WAVES * 64)) return KQ_ERR_UNSUPPORTED;
@@ -573,8 +574,8 @@ kq_status launch_tile(const GroupedArgs &a, hipStream_t s) {
 // rows, E groups):
 //   the stream kernel, where 128 x 128 tiles are too few to keep the card's loads going and the
 //   rows too few to ask for more than loads, or where such tiles are very few:
-//     R 8, E 8, N 4096, K 4096 INT8 (256 tiles of 128): 16.7 against 24.6; R 64: 25.4, 32.5;
-//     R 2040, E 2, N 88, K 8576 INT4 (17 tiles): 21 against 45;
+//     R 8, E 8, N 4096, K 4096 INT8 (256 tiles of 128): 16.5 against 24.6; R 64: 26.9, 32.5;
+//     R 2040, E 2, N 88, K 8576 INT4 (17 tiles): 10.4 against 45;
 //     but R 256, E 32, N 2048, K 7168 INT8 (544 tiles): 104 against 82; R 300, E 2, N 4096,
 //     K 4096 INT8 (128 tiles, 150 rows a group): 43 against 34;
 //   256 x 256 tiles, where the groups fill them and there are enough for the 256 compute units:
@@ -587,7 +588,8 @@ kq_status launch(const GroupedArgs &a, hipStream_t s) {
   const int64_t groups = a.R < a.E ? a.R : a.E, per_group = a.R / groups;
   const int64_t tiles128 = (a.N + 127) / 128 * (a.R / 128 + groups);
   const int64_t tiles256 = (a.N + 255) / 256 * (a.R / 256 + groups);
-  if (tiles128 < 64 || (tiles128 < 512 && per_group <= 16)) return launch_stream<BITS>(a, s);
+  if (tiles128 < 64 || (tiles128 < 512 && per_group <= 16))
+    return per_group <= 8 ? launch_stream<BITS, 1>(a, s) : launch_stream<BITS, 2>(a, s);
   if (per_group >= 96 && tiles256 >= 192) return launch_tile<BITS, 256>(a, s);
   return launch_tile<BITS, 128>(a, s);
 }
