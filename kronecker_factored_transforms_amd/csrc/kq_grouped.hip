@@ -301,14 +301,27 @@ struct Tiling : Share<BITS, SIDE> {
   typedef Share<BITS, SIDE> S;
   static constexpr int kWaves = S::kWM * S::kWN;
   static constexpr int kMI = SIDE / S::kWM / S::kSide, kApart = S::kWN * S::kSide, kBlocks = SIDE / kApart;
-  static constexpr int kOpBytes = SIDE * kStep;  // per operand and buffer, two buffers
+  static constexpr int kOpBytes = SIDE * kStep;  // per operand and step in LDS
   static constexpr int kOutBytes = 2 * kApart * (SIDE * 4 + 16);  // two blocks of fp32 output rows
-  static constexpr int kLds = 4 * kOpBytes > kOutBytes ? 4 * kOpBytes : kOutBytes;
+  template <int STAGES>
+  static constexpr int kLds = STAGES * 2 * kOpBytes > kOutBytes ? STAGES * 2 * kOpBytes : kOutBytes;
   static constexpr int kLoads = kOpBytes / 1024 / kWaves;
   static_assert(kLoads * 1024 * kWaves == kOpBytes, "the tile splits evenly over the waves");
 };
 
-template <int BITS, int SIDE, int OUT, int NU>
+// Wait until at most min(left, MOST) later steps of LOADS loads each are still on their way
+template <int LOADS, int MOST>
+__device__ __forceinline__ void wait_steps(int left) {
+  static_assert(LOADS * MOST < 64, "fits the wait counter");
+  if constexpr (MOST == 0) {
+    wait_and_fence<kWaitVm0>();
+  } else {
+    if (left >= MOST) wait_and_fence<wait_vm_imm(LOADS * MOST)>();
+    else wait_steps<LOADS, MOST - 1>(left);
+  }
+}
+
+template <int BITS, int SIDE, int STAGES, int OUT, int NU>
 __device__ __forceinline__ void tile_product(const GroupedArgs &p, const RowTile &tile, int64_t n0,
                                              unsigned char *s_buf, unsigned char *s_ok) {
   typedef Tiling<BITS, SIDE> S;
@@ -435,29 +448,34 @@ __device__ __forceinline__ void tile_product(const GroupedArgs &p, const RowTile
     __builtin_amdgcn_sched_barrier(0);
     asm volatile("" ::: "memory");
   };
-  dma_step(0, 0);
   if constexpr (BITS == 4) {
-    // two waves of a SIMD cover each other's reads; a second part in registers would not fit
-    for (int ks = 0; ks < steps; ++ks) {
-      wait_and_fence<kWaitVm0>();
-      sync();  // this step has landed for every wave, and every wave is done with the one before
-      if (ks + 1 < steps) dma_step(ks + 1, (ks + 1) & 1);
+    // the unpacking between reads and products covers the reads; a second part in registers costs
+    // more than it gives (256: it spills, 2042 against 841 us; 128: 67 against 63 us on R 8192,
+    // N 512, K 8192)
 #pragma unroll
-      for (int q = 0; q < kParts; ++q) multiply(read_part(buf(ks & 1), q));
+    for (int k = 0; k < STAGES - 1; ++k)
+      if (k < steps) dma_step(k, k);
+    int b = 0;  // this step's buffer
+    for (int ks = 0; ks < steps; ++ks) {
+      wait_steps<2 * kLoads, STAGES - 2>(steps - 1 - ks);
+      sync();  // this step has landed for every wave, and every wave is done with the one before
+      if (ks + STAGES - 1 < steps) dma_step(ks + STAGES - 1, b == 0 ? STAGES - 1 : b - 1);
+#pragma unroll
+      for (int q = 0; q < kParts; ++q) multiply(read_part(buf(b), q));
       wait_and_fence<kWaitLgkm0>();
+      b = b + 1 == STAGES ? 0 : b + 1;
     }
   } else {
     // each part is read while the one before it multiplies, across the steps
-    if (steps > 1) {
-      dma_step(1, 1);
-      wait_and_fence<wait_vm_imm(2 * kLoads)>();
-    } else {
-      wait_and_fence<kWaitVm0>();
-    }
+#pragma unroll
+    for (int k = 0; k < STAGES; ++k)
+      if (k < steps) dma_step(k, k);
+    wait_steps<2 * kLoads, STAGES - 1>(steps - 1);
     sync();
     Part f = read_part(buf(0), 0);
+    int b = 0;  // this step's buffer
     for (int ks = 0; ks < steps; ++ks) {
-      const int b = ks & 1;
+      const int after = b + 1 == STAGES ? 0 : b + 1;
 #pragma unroll
       for (int q = 0; q < kParts; ++q) {
         Part next = f;
@@ -466,18 +484,19 @@ __device__ __forceinline__ void tile_product(const GroupedArgs &p, const RowTile
         } else if (ks + 1 < steps) {
           // this wave's reads of buffer b have returned, and its loads of the next step have
           // landed; behind the barrier that holds for every wave, so b may be overwritten and
-          // the other buffer read
+          // the next buffer read
           wait_and_fence<kWaitLgkm0>();
-          wait_and_fence<kWaitVm0>();
+          wait_steps<2 * kLoads, STAGES - 2>(steps - 2 - ks);
           sync();
-          next = read_part(buf(b ^ 1), 0);
-          if (ks + 2 < steps) dma_step(ks + 2, b);
+          next = read_part(buf(after), 0);
+          if (ks + STAGES < steps) dma_step(ks + STAGES, b);
         }
         __builtin_amdgcn_sched_barrier(0);
         multiply(f);
         __builtin_amdgcn_sched_barrier(0);
         f = next;
       }
+      b = after;
     }
   }
 
@@ -488,7 +507,7 @@ __device__ __forceinline__ void tile_product(const GroupedArgs &p, const RowTile
   constexpr int kQ = S::kMI * kRegs / 4;  // groups of 4 channels
   constexpr int kSize = OUT == KQ_FP32 ? 4 : 2, kRowBytes = SIDE * kSize + 16;
   constexpr int kRowLanes = SIDE * kSize / 16, kAtOnce = 64 / kRowLanes, kPer = 16 / kSize;
-  static_assert(2 * S::kApart * kRowBytes <= S::kLds, "two places of rows");
+  static_assert(2 * S::kApart * kRowBytes <= S::template kLds<STAGES>, "two places of rows");
   const int ml = wm * (SIDE / S::kWM) + 4 * g;  // this lane's channels: ml + group_at(q)
   auto group_at = [](int q) { return q / (kRegs / 4) * S::kSide + q % (kRegs / 4) * 4 * (64 / S::kSide); };
   float sw[kQ][4];
@@ -523,23 +542,23 @@ __device__ __forceinline__ void tile_product(const GroupedArgs &p, const RowTile
   }
 }
 
-template <int BITS, int SIDE, int OUT>
+template <int BITS, int SIDE, int STAGES, int OUT>
 __global__ __launch_bounds__((Tiling<BITS, SIDE>::kWaves * 64)) void kq_grouped_tile_kernel(const GroupedArgs p, int tiles_m) {
   typedef Tiling<BITS, SIDE> S;
-  __shared__ __align__(16) unsigned char s_buf[S::kLds];
+  __shared__ __align__(16) unsigned char s_buf[S::template kLds<STAGES>];
   __shared__ unsigned char s_ok[SIDE];  // which rows of the tile are written
   const RowTile tile = find_tile<SIDE>(p.offsets, p.E, p.R, (int)(blockIdx.x / tiles_m));
   if (tile.e < 0) return;
   const int64_t n0 = (int64_t)(blockIdx.x % tiles_m) * SIDE;
   if constexpr (S::kBlocks == 4) {
-    if (tile.count > 3 * S::kApart) tile_product<BITS, SIDE, OUT, 4>(p, tile, n0, s_buf, s_ok);
-    else if (tile.count > 2 * S::kApart) tile_product<BITS, SIDE, OUT, 3>(p, tile, n0, s_buf, s_ok);
-    else if (tile.count > S::kApart) tile_product<BITS, SIDE, OUT, 2>(p, tile, n0, s_buf, s_ok);
-    else tile_product<BITS, SIDE, OUT, 1>(p, tile, n0, s_buf, s_ok);
+    if (tile.count > 3 * S::kApart) tile_product<BITS, SIDE, STAGES, OUT, 4>(p, tile, n0, s_buf, s_ok);
+    else if (tile.count > 2 * S::kApart) tile_product<BITS, SIDE, STAGES, OUT, 3>(p, tile, n0, s_buf, s_ok);
+    else if (tile.count > S::kApart) tile_product<BITS, SIDE, STAGES, OUT, 2>(p, tile, n0, s_buf, s_ok);
+    else tile_product<BITS, SIDE, STAGES, OUT, 1>(p, tile, n0, s_buf, s_ok);
   } else {
     static_assert(S::kBlocks == 2, "blocks of a wave");
-    if (tile.count > S::kApart) tile_product<BITS, SIDE, OUT, 2>(p, tile, n0, s_buf, s_ok);
-    else tile_product<BITS, SIDE, OUT, 1>(p, tile, n0, s_buf, s_ok);
+    if (tile.count > S::kApart) tile_product<BITS, SIDE, STAGES, OUT, 2>(p, tile, n0, s_buf, s_ok);
+    else tile_product<BITS, SIDE, STAGES, OUT, 1>(p, tile, n0, s_buf, s_ok);
   }
 }
 
@@ -554,7 +573,7 @@ kq_status launch_stream(const GroupedArgs &a, hipStream_t s) {
   return hipGetLastError() == hipSuccess ? KQ_OK : KQ_ERR_HIP;
 }
 
-template <int BITS, int SIDE>
+template <int BITS, int SIDE, int STAGES>
 kq_status launch_tile(const GroupedArgs &a, hipStream_t s) {
   constexpr int kThreads = Tiling<BITS, SIDE>::kWaves * 64;
   const int64_t tiles_m = (a.N + SIDE - 1) / SIDE;
@@ -562,11 +581,11 @@ kq_status launch_tile(const GroupedArgs &a, hipStream_t s) {
   if (tiles_m * tiles > 0x7FFFFFFF / kThreads) return KQ_ERR_UNSUPPORTED;
   const dim3 grid((unsigned)(tiles_m * tiles)), block(kThreads);
   if (a.out_dtype == KQ_FP32)
-    hipLaunchKernelGGL((kq_grouped_tile_kernel<BITS, SIDE, KQ_FP32>), grid, block, 0, s, a, (int)tiles_m);
+    hipLaunchKernelGGL((kq_grouped_tile_kernel<BITS, SIDE, STAGES, KQ_FP32>), grid, block, 0, s, a, (int)tiles_m);
   else if (a.out_dtype == KQ_BF16)
-    hipLaunchKernelGGL((kq_grouped_tile_kernel<BITS, SIDE, KQ_BF16>), grid, block, 0, s, a, (int)tiles_m);
+    hipLaunchKernelGGL((kq_grouped_tile_kernel<BITS, SIDE, STAGES, KQ_BF16>), grid, block, 0, s, a, (int)tiles_m);
   else
-    hipLaunchKernelGGL((kq_grouped_tile_kernel<BITS, SIDE, KQ_FP16>), grid, block, 0, s, a, (int)tiles_m);
+    hipLaunchKernelGGL((kq_grouped_tile_kernel<BITS, SIDE, STAGES, KQ_FP16>), grid, block, 0, s, a, (int)tiles_m);
   return hipGetLastError() == hipSuccess ? KQ_OK : KQ_ERR_HIP;
 }
 
@@ -582,7 +601,10 @@ kq_status launch_tile(const GroupedArgs &a, hipStream_t s) {
 //     R 16384, E 8, N 14336, K 4096: INT4 858 against 911, INT8 1054 against 1254;
 //     but R 8192, E 4, N 512, K 8192 INT8 (72 tiles of 256): 110 against 73; R 2048, E 64,
 //     N 4096, K 7168 INT4 (32 rows a group): 222 against 182;
-//   128 x 128 tiles otherwise (two workgroups of them share a compute unit).
+//   128 x 128 tiles otherwise; two workgroups of them share a compute unit. Up to 256 of them each
+//   has one to itself, and four steps in LDS: R 128, E 4, N 4096, K 4096 INT8 23.5 against 35.3,
+//   R 2000, E 8, N 1024, K 2048 16.3 against 17.4 (INT4 within 3 %); but R 8192, E 4, N 512,
+//   K 8192 INT8 (272 tiles) 83 against 72.
 template <int BITS>
 kq_status launch(const GroupedArgs &a, hipStream_t s) {
   const int64_t groups = a.R < a.E ? a.R : a.E, per_group = a.R / groups;
@@ -590,8 +612,8 @@ kq_status launch(const GroupedArgs &a, hipStream_t s) {
   const int64_t tiles256 = (a.N + 255) / 256 * (a.R / 256 + groups);
   if (tiles128 < 64 || (tiles128 < 512 && per_group <= 16))
     return per_group <= 8 ? launch_stream<BITS, 1>(a, s) : launch_stream<BITS, 2>(a, s);
-  if (per_group >= 96 && tiles256 >= 192) return launch_tile<BITS, 256>(a, s);
-  return launch_tile<BITS, 128>(a, s);
+  if (per_group >= 96 && tiles256 >= 192) return launch_tile<BITS, 256, 2>(a, s);
+  return tiles128 <= 256 ? launch_tile<BITS, 128, 4>(a, s) : launch_tile<BITS, 128, 2>(a, s);
 }
 
 constexpr int64_t kMax31 = 0x7FFFFFFF;
