@@ -305,9 +305,11 @@ def _elsewhere(device, stream):
 
 
 def _current(index) -> int:
-    """Handle of device `index`'s current stream."""
+    """Handle of device `index`'s current stream (the short way where torch has it: a tenth of a
+    microsecond instead of three)."""
     import torch
-    return torch._C._cuda_getCurrentRawStream(index)
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(index) if raw else int(torch.cuda.current_stream(index).cuda_stream)
 
 
 def _need(ok, what):

@@ -88,7 +88,32 @@ def test_shapes(gpu, dtype, T, K, N, r, L):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("T", [40, 900])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("r", [8, 16, 32, 56, 64, 120, 128, 256])
+@pytest.mark.parametrize("T", [1024, 1337, 4096, 4133])
+def test_many_tokens(gpu, T, r, dtype):
+    """The two ways of many tokens (parts joined in between; K whole), prompts whose ends fall
+    inside tiles of 16 and 32."""
+    import torch
+    seg = torch.arange(T) // 205 % 5 - 1
+    a = _inputs(gpu, T, 328, 200, r, 4, dtype, seed=r + T, adapter=seg)
+    _check(*a, B.adapter_add(*a[:4], base=a[4], scaling=a[5]))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,gain", [("bf16", 1.0), ("fp16", 1e-5), ("fp16", 200.0)])
+@pytest.mark.parametrize("T", [1500, 5000])
+def test_many_tokens_in_any_order(gpu, T, dtype, gain):
+    """Every adapter in every tile, K past one step per wave, h of any size."""
+    a = _inputs(gpu, T, 2056, 136, 24, 19, dtype, seed=T, gain=gain)
+    _check(*a, B.adapter_add(*a[:4], base=a[4], scaling=a[5]))
+    base = a[4].clone()
+    out = B.adapter_add(*a[:4], base=base, scaling=a[5], out=base)
+    _check(*a, out)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [40, 900, 1100, 4200])
 def test_orders_of_adapters(gpu, T):
     """All tokens on one adapter, none on any, every token another, and segments whose ends
     fall inside tiles; numbers outside 0 .. L-1 name none."""
@@ -129,7 +154,7 @@ def test_no_base_no_scaling_and_in_place(gpu, T):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("T", [20, 500])
+@pytest.mark.parametrize("T", [20, 500, 1200, 4111])
 def test_strides(gpu, T):
     import torch
     x, A, Bm, ad, base, s = _inputs(gpu, T, 264, 136, 24, 3, "fp16", seed=5)
@@ -147,7 +172,7 @@ def test_strides(gpu, T):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("T", [16, 48, 800])
+@pytest.mark.parametrize("T", [16, 48, 800, 1030, 4100])
 def test_what_is_not_finite_stays_with_its_own_tokens(gpu, T):
     """NaN and infinities in one adapter, and in one token's row, reach no other token."""
     import torch
@@ -170,11 +195,12 @@ def test_what_is_not_finite_stays_with_its_own_tokens(gpu, T):
 
 
 @pytest.mark.gpu
-def test_another_stream_and_captured_calls(gpu):
+@pytest.mark.parametrize("T", [70, 1025, 4097])
+def test_another_stream_and_captured_calls(gpu, T):
     """Two graphs in turn, each with a workspace of its own, follow the adapters of each replay."""
     import torch
     L = 6
-    sets = [_inputs(gpu, 70, 512, 264, 16, L, "bf16", seed=i) for i in range(4)]
+    sets = [_inputs(gpu, T, 512, 264, 16, L, "bf16", seed=i) for i in range(4)]
     x, A, Bm, ad, base, s = sets[0]
     want = [B.adapter_add(t[0], A, Bm, t[3], base=t[4], scaling=s) for t in sets]
     torch.cuda.synchronize()

@@ -160,6 +160,61 @@ def test_strides(gpu, bits, counts):
             assert bool((big[:, :lead] == 3).all()) and bool((big[:, lead + N:] == 3).all())
 
 
+def _counts(rng, E, mean):
+    """Ragged groups around a mean, an empty one and a single row among them."""
+    c = rng.integers(mean // 2, mean * 3 // 2, E)
+    c[1], c[2] = 0, 1
+    return [int(v) for v in c]
+
+
+# One shape for each kernel and number of steps in LDS, by the rule that picks them: enough 256 x
+# 256 tiles; 128 x 128 tiles, more than 256 of them and fewer; few rows over many groups; tiny N.
+PICKED = {"tiles256": (16, 170, 2053), "tiles128": (40, 50, 1003), "few tiles128": (6, 60, 1500),
+          "rows of decode": (30, 5, 3100), "stream": (9, 7, 700), "stream32": (3, 400, 70)}
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("out_dtype", ["fp32", "bf16", "fp16"])
+@pytest.mark.parametrize("name", PICKED)
+@pytest.mark.parametrize("K", [32, 512, 1056])
+def test_every_kernel(gpu, name, K, out_dtype, bits):
+    E, mean, N = PICKED[name]
+    rng = np.random.default_rng(E + K + bits)
+    counts = _counts(rng, E, mean)
+    R = sum(counts) + 2
+    case = _case(rng, 500, K, E, N, counts, bits, np.float16 if bits == 4 else np.float32)
+    src = np.concatenate([case[5], [0, 0]]).astype(np.int32)
+    src[::37] = -1  # padding rows
+    case = (*case[:5], src)
+    _same(_run(gpu, case, bits, out_dtype, R), _want(*case, None, R))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("name", ["tiles256", "tiles128", "few tiles128", "stream"])
+def test_every_kernel_largest_sums_and_odd_rows(gpu, name, bits):
+    """The largest sums of a long K (the kernels' last step cut short), and outputs at odd
+    addresses."""
+    import torch
+    E, mean, N = PICKED[name]
+    rng = np.random.default_rng(E)
+    counts = _counts(rng, E, mean)
+    R, Kc = sum(counts), 16384 + 32
+    qx, qw, sx, sw, off, src = _case(rng, 4, Kc, E, N, counts, bits, np.float32, extremes=True)
+    dev = lambda a: torch.from_numpy(np.ascontiguousarray(a)).to(gpu)  # noqa: E731
+    big = torch.full((R, N + 3), 3.0, dtype=torch.bfloat16, device=gpu)
+    wq = dev(_pack(qw.reshape(-1, Kc), bits)).view(E, N, -1)
+    B.grouped_gemm(dev(_pack(qx, bits)), dev(sx), wq, dev(sw), dev(off), rows=dev(src), bits=bits,
+                   out_dtype="bf16", out=big[:, 1:N + 1])
+    torch.cuda.synchronize()
+    lo = -8 if bits == 4 else -128
+    e = np.repeat(np.arange(E), counts)  # every sum is the same: K lo^2
+    want = np.float32(Kc * lo * lo) * sx[src][:, None] * sw[e]
+    _same(big[:, 1:N + 1], want)
+    assert bool((big[:, 0] == 3).all()) and bool((big[:, N + 1:] == 3).all())
+
+
 @pytest.mark.gpu
 def test_one_group_is_the_dense_product(gpu):
     """One group of all rows: kq_int4_gemm's result, bit for bit."""
