@@ -20,8 +20,8 @@
 // of a prompt stand together, so most of its blocks have one adapter; the many of a decode
 // batch's blocks are loaded several at a time.
 #include "kq_internal.h"
-#include "kq_common.h"
 #include "kq_device.h"
+#include "kq_linear.h"
 
 namespace {
 
@@ -136,14 +136,6 @@ __device__ __forceinline__ void store_operands(const AdapterArgs &p, int64_t til
 }
 
 constexpr int kStep = 64;  // values of K per step: rows of 128 bytes in LDS
-__device__ __align__(16) const unsigned char kZeroPiece[16] = {};
-
-__device__ __forceinline__ const unsigned char *uniform(const void *p) {
-  const uint64_t v = reinterpret_cast<uint64_t>(p);
-  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v);
-  const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
-  return reinterpret_cast<const unsigned char *>((uint64_t)hi << 32 | lo);
-}
 
 // The products of DD adapters' A (numbers a[]) with TF blocks of 16 tokens, over one wave's steps
 // s0, s0 + WAVES, .. of K below s1; RB blocks of 16 ranks. Rows come by DMA into the wave's own
@@ -199,12 +191,12 @@ __device__ __forceinline__ void down_product(const AdapterArgs &p, int64_t t0, c
     } else {  // the rows end inside this step: the rest comes from a block of zeros
 #pragma unroll
       for (int j = 0; j < kX; ++j)
-        dma16_addr<false>(s * 8 + piece[j % 2] < pieces ? x + o + vx[j] : kZeroPiece, lds_addr(to + j * 1024));
+        dma16_addr<false>(s * 8 + piece[j % 2] < pieces ? x + o + vx[j] : kZeros, lds_addr(to + j * 1024));
 #pragma unroll
       for (int d = 0; d < DD; ++d)
 #pragma unroll
         for (int j = 0; j < kA; ++j)
-          dma16_addr<false>(s * 8 + piece[j % 2] < pieces ? am[d] + o + va[j] : kZeroPiece,
+          dma16_addr<false>(s * 8 + piece[j % 2] < pieces ? am[d] + o + va[j] : kZeros,
                             lds_addr(to + (kX + d * kA + j) * 1024));
     }
   };

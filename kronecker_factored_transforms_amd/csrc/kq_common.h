@@ -66,14 +66,6 @@ __device__ __forceinline__ float wave_max_uniform(float v) {
   return max_nn(max_nn(r0, r1), max_nn(r2, r3));
 }
 
-// fp32 -> fp16, round to nearest even, of the fp32 value as it stands: the value is opaque to
-// the compiler, which would otherwise fold a preceding product or sum into an instruction that
-// rounds its exact result to fp16 at once (one rounding instead of the two that are meant).
-__device__ __forceinline__ _Float16 half_rne(float v) {
-  asm("" : "+v"(v));
-  return (_Float16)v;
-}
-
 __device__ __forceinline__ bf16x8 pack8(const f32x4 &a, const f32x4 &b) {
   bf16x8 r;
   r[0] = (__bf16)a[0]; r[1] = (__bf16)a[1]; r[2] = (__bf16)a[2]; r[3] = (__bf16)a[3];

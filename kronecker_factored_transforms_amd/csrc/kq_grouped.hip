@@ -16,8 +16,8 @@
 // unpacking; INT8 reads twice the bytes from LDS, whose writes and reads take as long as its
 // products.
 #include "kq_internal.h"
-#include "kq_common.h"
 #include "kq_device.h"
+#include "kq_linear.h"
 
 namespace {
 
@@ -260,16 +260,6 @@ __global__ __launch_bounds__(WAVES * 64) void kq_grouped_stream_kernel(const Gro
 constexpr int kStep = 128;  // bytes of every row per step of the reduction
 
 typedef int i32x16 __attribute__((ext_vector_type(16)));
-
-__device__ __align__(16) const unsigned char kZeros[16] = {};
-
-// The same address, in scalar registers (it is the same in every lane)
-__device__ __forceinline__ const uint8_t *uniform(const uint8_t *p) {
-  const uint64_t v = reinterpret_cast<uint64_t>(p);
-  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v);
-  const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
-  return reinterpret_cast<const uint8_t *>((uint64_t)hi << 32 | lo);
-}
 
 // 16 int8 operand bytes from one dword pair of INT4 codes (16 codes)
 __device__ __forceinline__ i32x4 unpack16(unsigned x, unsigned y) {

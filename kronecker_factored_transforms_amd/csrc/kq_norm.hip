@@ -12,7 +12,7 @@
 // bytes per bf16 value). 16384 x 8192 bf16 with a residual: 163-166 us, 5.7 TB/s, where a
 // device-to-device copy of the same size reaches 5.2.
 #include "kq_internal.h"
-#include "kq_common.h"
+#include "kq_linear.h"
 
 namespace {
 
