@@ -314,8 +314,8 @@ kq_status kq_weight_factor(const void *P, int m, kq_dtype dtype, void *out, void
  *              itself (same address and stride).
  *   codes      device, T x n bytes, row stride n, or NULL.
  *   scales     device, T steps of scale_dtype (KQ_FP16 or KQ_FP32); NULL exactly with codes.
- * At least one of codes and normed is given. n is 1 .. 65536; rows that are 16-byte aligned
- * with n a multiple of 8 move 16 bytes at a time, others one value at a time. Outputs may not
+ * At least one of codes and normed is given. n is 1 .. 65536; rows may start at any multiple
+ * of their type's size (16-byte aligned ones are a little faster). Outputs may not
  * overlap each other, nor inputs but as said above. The sum of squares is held in fp32: rows
  * whose sum is not finite give unspecified outputs (as non-finite inputs do). T == 0 returns
  * KQ_OK and launches nothing. Asynchronous on `stream`; no allocation. Errors: INVALID_ARG
@@ -345,17 +345,18 @@ kq_status kq_rmsnorm_quant(const void *x, int64_t ldx, const void *residual, int
  *            row stride ldwq bytes; 16-byte aligned, ldwq and ldwe multiples of 16.
  *   sw       device, E x N steps of scale_dtype, contiguous.
  *   offsets  device, E + 1 values, not decreasing, in 0 .. R (values outside are taken as the
- *            nearer end, a decrease as an empty group). Output rows outside every group are
- *            left as they were.
+ *            nearer end). Where they decrease all the same, what out's rows hold afterwards is
+ *            unspecified. Output rows outside every group are left as they were.
  *   bits     4 or 8.
  *   K        codes per row: K * bits / 8 a multiple of 16 bytes, K at most 65536.
  *   out      device, R rows of N values of out_dtype (KQ_FP32, KQ_BF16, KQ_FP16), row stride
- *            ldo elements.
- * E is 1 .. 4096. R == 0 or N == 0 returns KQ_OK and launches nothing. The call does not read
+ *            ldo elements; no input.
+ * E is 1 .. 4096. R == 0 or N == 0 returns KQ_OK and launches nothing (T is at least 1
+ * otherwise). The call does not read
  * offsets or rows on the host, so their values may change between replays of a captured
  * graph. Asynchronous on `stream`; no allocation. Errors: INVALID_ARG (NULLs, sizes, strides
- * too small, bits, dtypes), UNSUPPORTED (K or E not as above, a row stride of wq of 16 MiB or
- * more, sizes or strides of 2^31 or more), ALIGNMENT, HIP.
+ * too small, bits, dtypes, overlaps), UNSUPPORTED (K or E not as above, a row stride of wq of
+ * 16 MiB or more, sizes or strides of 2^31 or more), ALIGNMENT, HIP.
  */
 kq_status kq_grouped_gemm(const uint8_t *xq, int64_t ldxq, const void *sx, int64_t T,
                           const int32_t *rows, int64_t R, const uint8_t *wq, int64_t ldwq,
@@ -382,8 +383,8 @@ kq_status kq_grouped_gemm(const uint8_t *xq, int64_t ldxq, const void *sx, int64
  *            (same address and stride), but no other input.
  *   K, N, r  multiples of 8; K and N at most 2^20, r at most 256. L >= 1.
  *   workspace  device, at least kq_adapter_workspace_size(T, K, r) bytes, 256-byte aligned;
- *            its contents on entry do not matter. Calls that share a workspace must be
- *            ordered (same stream), or they race on it.
+ *            its contents on entry do not matter; it overlaps no other argument. Calls that
+ *            share a workspace must be ordered (same stream), or they race on it.
  * T == 0 or N == 0 returns KQ_OK and launches nothing. Asynchronous on `stream`; no
  * allocation; the result does not depend on the order of the sums' parts (no atomics).
  * Errors: INVALID_ARG (NULLs, sizes, strides too small, dtype, overlaps), UNSUPPORTED

@@ -647,6 +647,13 @@ static kq_status grouped_gemm_impl(const uint8_t *xq, int64_t ldxq, const void *
     return KQ_ERR_ALIGNMENT;
   if (off(sx, ss) || off(sw, ss) || off(out, os) || off(rows, 4) || off(offsets, 4))
     return KQ_ERR_ALIGNMENT;
+  const int64_t wb = (E - 1) * ldwe * (E > 1) + (N - 1) * ldwq + rb;
+  const kq_span o = kq_rows_span(out, R, ldo, N, os);
+  const kq_span in[6] = {kq_rows_span(xq, T, ldxq, rb, 1), kq_rows_span(sx, 1, T, T, ss),
+                         kq_rows_span(rows, 1, R, R, 4), kq_rows_span(wq, 1, wb, wb, 1),
+                         kq_rows_span(sw, 1, E * N, E * N, ss), kq_rows_span(offsets, 1, E + 1, E + 1, 4)};
+  for (const kq_span &i : in)
+    if (kq_overlap(o, i)) return KQ_ERR_INVALID_ARG;
   const GroupedArgs a = {xq, wq, sx, sw, rows, offsets, out, ldxq, ldwq, E > 1 ? ldwe : 0, T, R, N, ldo,
                          (int)(rb / 16), (int)E, scale_dtype == KQ_FP16 ? 1 : 0, (int)out_dtype};
   hipStream_t s = static_cast<hipStream_t>(stream);

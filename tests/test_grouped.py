@@ -342,3 +342,27 @@ def test_tensors_that_do_not_fit_are_refused(gpu):
         with pytest.raises(ValueError):
             B.grouped_gemm(**{**ok, "bits": 8, **kw})
     assert B.grouped_gemm(**ok, rows=torch.zeros(0, dtype=i32, device=gpu), bits=8).shape == (0, 8)
+
+
+def test_outputs_over_inputs_are_refused():
+    apart = dict(xq=0x10000, sx=0x20000, rows=0x30000, wq=0x40000, sw=0x50000, off=0x60000)
+    for name, at in apart.items():
+        assert _raw(**{**apart, "out": at}) == B.KQ_ERR_INVALID_ARG, name
+    # the last value of 16 rows of 32 (0x400 bytes), the last weight of 4 experts (0x4000 bytes)
+    assert _raw(**{**apart, "out": 0x20000 - 0x3fe}) == B.KQ_ERR_INVALID_ARG
+    assert _raw(**{**apart, "out": 0x44000 - 2}) == B.KQ_ERR_INVALID_ARG
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("mean", [2, 70, 300])
+def test_decreasing_offsets_stay_inside(gpu, mean, bits):
+    """Groups that overlap leave unspecified rows, but none outside the groups' range."""
+    import torch
+    rng = np.random.default_rng(mean + bits)
+    E, R = 6, 6 * mean
+    case = _case(rng, R, 512, E, 300, [mean] * E, bits, np.float32)
+    off = np.array([mean, 4 * mean, 2 * mean, 5 * mean, 3 * mean, 3 * mean, 4 * mean], np.int32)
+    out = _run(gpu, (*case[:4], off, case[5]), bits, "fp32", R).cpu()
+    assert (out[:mean] == -7.0).all() and (out[5 * mean:] == -7.0).all()
+    assert torch.isfinite(out).all()
