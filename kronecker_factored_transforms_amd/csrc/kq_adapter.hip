@@ -695,6 +695,10 @@ static kq_status adapter_add_impl(const void *x, int64_t ldx, const void *A, con
   const int64_t need = workspace_bytes(T, K, r);
   if (!workspace || ws_bytes < (size_t)need) return KQ_ERR_WORKSPACE;
   if (off(workspace, 256)) return KQ_ERR_ALIGNMENT;
+  const kq_span ws = kq_rows_span(workspace, 1, need, need, 1);
+  for (const kq_span &i : in)
+    if (kq_overlap(ws, i)) return KQ_ERR_INVALID_ARG;
+  if (kq_overlap(ws, o) || kq_overlap(ws, b)) return KQ_ERR_INVALID_ARG;
   const int splits = split_count(T, K), steps = (int)((K + kStep - 1) / kStep);
   const AdapterArgs a = {x, A, B, base, adapter, scaling, out, static_cast<float *>(workspace),
                          static_cast<char *>(workspace) + part_bytes(T, K, r), ldx, ldb, ldo, T, (int)K,

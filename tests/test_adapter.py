@@ -299,3 +299,10 @@ def test_tensors_that_do_not_fit_are_refused(gpu):
         with pytest.raises(ValueError):
             B.adapter_add(**{**ok, **kw})
     assert B.adapter_add(x[:0], A, Bm, ad[:0], base=base[:0]).shape == (0, 32)
+
+
+def test_workspace_over_other_arguments_is_refused():
+    for at in (0x10000, 0x20000, 0x30000, 0x40000, 0x50000, 0x60000, 0x70000):
+        assert _raw(ws=at) == B.KQ_ERR_INVALID_ARG, hex(at)
+    # 4 tokens of 16 ranks in fp32, one part: 0x100 bytes, so its last 16 are the first of out
+    assert _raw(ws=0x80000 - 0x100, out=0x80000 - 0x10) == B.KQ_ERR_INVALID_ARG
