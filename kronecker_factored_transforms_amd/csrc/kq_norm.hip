@@ -310,9 +310,8 @@ static kq_status rmsnorm_quant_impl(const void *x, int64_t ldx, const void *resi
   if (ldx < n || (residual && ldr < n) || (res_out && ldres < n) || (normed && ldy < n))
     return KQ_ERR_INVALID_ARG;
   const int64_t kMaxLd = (int64_t)1 << 40;
-  if (ldx > kMaxLd || ldr > kMaxLd || ldres > kMaxLd || ldy > kMaxLd ||
-      (T > 1 && (double)T * (double)(ldx > ldr ? ldx : ldr) > 4e18))
-    return KQ_ERR_INVALID_ARG;
+  for (const int64_t ld : {ldx, ldr, ldres, ldy})  // no product of a row and a stride passes 2^62
+    if (ld > kMaxLd || (T > 1 && (double)T * (double)ld > 1e18)) return KQ_ERR_INVALID_ARG;
   const size_t es = x_dtype == KQ_FP32 ? 4 : 2;
   if (off(x, es) || off(residual, es) || off(w, es) || off(res_out, es) || off(normed, es) ||
       off(scales, scale_dtype == KQ_FP32 ? 4 : 2))

@@ -272,3 +272,8 @@ def test_tensors_that_do_not_fit_are_refused(gpu):
             B.rmsnorm_quant(**a)
     e = B.rmsnorm_quant(x[:0], w, residual=r[:0], normed=True)
     assert e.codes.shape == (0, 64) and e.normed.shape == (0, 64)
+
+
+def test_strides_whose_rows_leave_64_bits_are_refused():
+    for name in ("ldx", "ldr", "ldres", "ldy"):
+        assert _raw(**{name: 1 << 40, "T": 1 << 30}) == B.KQ_ERR_INVALID_ARG, name
