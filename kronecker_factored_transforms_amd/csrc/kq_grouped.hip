@@ -323,7 +323,7 @@ __device__ __forceinline__ void tile_product(const GroupedArgs &p, const RowTile
                                              unsigned char *s_buf, unsigned char *s_ok) {
   typedef Tiling<BITS, SIDE> S;
   typedef typename S::acc_t acc_t;
-  constexpr int kOpBytes = S::kOpBytes, kLoads = S::kLoads;
+  constexpr int kOpBytes = S::kOpBytes, kLoads = S::kLoads, kXLoads = kLoads * NU / S::kBlocks;
   constexpr int kRegs = sizeof(acc_t) / 4;
   constexpr int kChunks = kStep / 16, kRowsPer = 1024 / kStep;
   const int lane = threadIdx.x & 63;
@@ -337,39 +337,46 @@ __device__ __forceinline__ void tile_product(const GroupedArgs &p, const RowTile
   // so that the rows of one fragment read spread over all banks. Rows past the end of the
   // weight or of the group read a valid row; their products are dropped.
   auto swz = [](int R) { return (R >> 1) & 7; };
-  const uint8_t *ax[kLoads];
+  auto row_of = [&](int loads, int j) { return (wave * loads + j) * kRowsPer + lane / kChunks; };
+  auto piece_of = [&](int loads, int j) { return (lane % kChunks) ^ swz(row_of(loads, j)); };
   const uint8_t *wbase = uniform(p.wq + tile.e * p.ldwe + n0 * p.ldwq);
   uint32_t vw[kLoads];  // 256 rows of at most 16 MiB (checked on the host): 32 bits
 #pragma unroll
   for (int j = 0; j < kLoads; ++j) {
-    const int R = (wave * kLoads + j) * kRowsPer + lane / kChunks;
-    const int piece = (lane % kChunks) ^ swz(R);
+    const int R = row_of(kLoads, j);
     const int64_t n = n0 + R < p.N ? R : p.N - 1 - n0;
-    vw[j] = (uint32_t)(n * p.ldwq + piece * 16);
+    vw[j] = (uint32_t)(n * p.ldwq + piece_of(kLoads, j) * 16);
+  }
+  const uint8_t *ax[kXLoads];  // of the NU blocks' rows
+#pragma unroll
+  for (int j = 0; j < kXLoads; ++j) {
+    const int R = row_of(kXLoads, j);
     int64_t t = tile.begin + (R < tile.count ? R : 0);
     if (p.rows) t = p.rows[t];
     if (t < 0 || t >= p.T) t = 0;
-    ax[j] = p.xq + t * p.ldxq + piece * 16;
+    ax[j] = p.xq + t * p.ldxq + piece_of(kXLoads, j) * 16;
   }
   const int steps = (p.pieces + kChunks - 1) / kChunks;
   auto dma_step = [&](int ks, int b) {
+    unsigned char *w_to = buf(b) + wave * (kLoads * 1024);
+    unsigned char *x_to = buf(b) + kOpBytes + wave * (kXLoads * 1024);
+    const uint8_t *w = wbase + (int64_t)ks * kStep;
     if ((ks + 1) * kChunks <= p.pieces) {
-      const uint8_t *w = wbase + (int64_t)ks * kStep;
 #pragma unroll
       for (int j = 0; j < kLoads; ++j) {
-        dma16<false>(w, vw[j], lds_addr(buf(b) + (wave * kLoads + j) * 1024));
-        dma16_addr<false>(ax[j], lds_addr(buf(b) + kOpBytes + (wave * kLoads + j) * 1024));
-        ax[j] += kStep;
+        dma16<false>(w, vw[j], lds_addr(w_to + j * 1024));
+        if (j < kXLoads) {
+          dma16_addr<false>(ax[j], lds_addr(x_to + j * 1024));
+          ax[j] += kStep;
+        }
       }
     } else {  // the last step of a row that ends inside it: the rest comes from a block of zeros
 #pragma unroll
-      for (int j = 0; j < kLoads; ++j) {
-        const int R = (wave * kLoads + j) * kRowsPer + lane / kChunks;
-        const bool in = ks * kChunks + ((lane % kChunks) ^ swz(R)) < p.pieces;
-        dma16_addr<false>(in ? wbase + (int64_t)ks * kStep + vw[j] : kZeros,
-                          lds_addr(buf(b) + (wave * kLoads + j) * 1024));
-        dma16_addr<false>(in ? ax[j] : kZeros, lds_addr(buf(b) + kOpBytes + (wave * kLoads + j) * 1024));
-      }
+      for (int j = 0; j < kLoads; ++j)
+        dma16_addr<false>(ks * kChunks + piece_of(kLoads, j) < p.pieces ? w + vw[j] : kZeros, lds_addr(w_to + j * 1024));
+#pragma unroll
+      for (int j = 0; j < kXLoads; ++j)
+        dma16_addr<false>(ks * kChunks + piece_of(kXLoads, j) < p.pieces ? ax[j] : kZeros, lds_addr(x_to + j * 1024));
     }
   };
 
@@ -454,7 +461,7 @@ __device__ __forceinline__ void tile_product(const GroupedArgs &p, const RowTile
       if (k < steps) dma_step(k, k);
     int b = 0;  // this step's buffer
     for (int ks = 0; ks < steps; ++ks) {
-      wait_steps<2 * kLoads, STAGES - 2>(steps - 1 - ks);
+      wait_steps<kLoads + kXLoads, STAGES - 2>(steps - 1 - ks);
       sync();  // this step has landed for every wave, and every wave is done with the one before
       if (ks + STAGES - 1 < steps) dma_step(ks + STAGES - 1, b == 0 ? STAGES - 1 : b - 1);
 #pragma unroll
@@ -467,7 +474,7 @@ __device__ __forceinline__ void tile_product(const GroupedArgs &p, const RowTile
 #pragma unroll
     for (int k = 0; k < STAGES; ++k)
       if (k < steps) dma_step(k, k);
-    wait_steps<2 * kLoads, STAGES - 1>(steps - 1);
+    wait_steps<kLoads + kXLoads, STAGES - 1>(steps - 1);
     sync();
     Part f = read_part(buf(0), 0);
     int b = 0;  // this step's buffer
@@ -483,7 +490,7 @@ __device__ __forceinline__ void tile_product(const GroupedArgs &p, const RowTile
           // landed; behind the barrier that holds for every wave, so b may be overwritten and
           // the next buffer read
           wait_and_fence<kWaitLgkm0>();
-          wait_steps<2 * kLoads, STAGES - 2>(steps - 2 - ks);
+          wait_steps<kLoads + kXLoads, STAGES - 2>(steps - 2 - ks);
           sync();
           next = read_part(buf(after), 0);
           if (ks + STAGES < steps) dma_step(ks + STAGES, b);
