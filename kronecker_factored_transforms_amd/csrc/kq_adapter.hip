@@ -9,10 +9,13 @@
 // up the parts.) Rounded to 16 bits, h would lose what fp32 sums gained: it enters the second
 // product as two 16-bit terms, hi + lo, on twice the instructions, which the memory's time hides.
 //
+// Up to 16 tokens on few small adapters take one kernel that does both (see there).
+//
 // Bound by memory for prompts (x, base and out once): 8192 tokens, K = N = 4096, r 16 48 us, 0.81
 // of the time that their bytes take at a copy's rate (5.2 TB/s); K 4096, N 14336, r 64 150 us,
 // 0.71: there h's operands, B and the products add to each wave's chain. By the two kernels'
-// latency for decode: 128 tokens on 32 adapters, r 16, K = N = 8192 18 us.
+// latency for decode: 128 tokens on 32 adapters, r 16, K = N = 8192 15.6 us;
+// one token, r 16, K = N = 4096 5.2 us.
 //
 // Both take blocks of 16 tokens as they stand: for each adapter that occurs among them, one
 // product of its matrix with all 16 columns, of which the tokens of that adapter keep theirs (a
@@ -562,6 +565,93 @@ __global__ __launch_bounds__(kUpWaves * 64) void kq_adapter_up_kernel(const Adap
   }
 }
 
+constexpr int kFewWaves = 8, kFewRing = 16 * 1024, kFewCols = 16 * kFewWaves;
+
+// Up to 16 tokens in one kernel: every workgroup forms the whole of h for itself (its waves split
+// K) and takes 16 columns a wave of the second product. A is read by all of them, from the caches;
+// what it saves is the second kernel's launch and the parts' way through memory.
+template <int DT, int RB>
+__global__ __launch_bounds__(kFewWaves * 64) void kq_adapter_few_kernel(const AdapterArgs p) {
+  typedef typename Half<DT>::vec vec;
+  typedef typename Half<DT>::one one;
+  constexpr int RS = (RB + 1) / 2, kRow = 32 * RS + 4;
+  typedef one one4 __attribute__((ext_vector_type(4)));
+  __shared__ __align__(16) unsigned char s_mem[kFewWaves * kFewRing];
+  __shared__ __align__(16) float s_h[16 * kRow];
+  f32x4 *s_acc = reinterpret_cast<f32x4 *>(s_mem);  // [kFewWaves][RB][64], behind the rings' use
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int g = lane >> 4, lr = lane & 15;
+  const int n0 = (int)(blockIdx.x * kFewWaves + wave) * 16;
+  const int l = token_adapter(p, lr);
+  // lane: columns c .. c+3 of token lr; its row of B; the ranks of its operands
+  const int c = n0 + 4 * g;
+  const bool live = c < p.N && lr < p.T;  // N is a multiple of 8
+  const uint32_t brow = (uint32_t)min(n0 + lr, p.N - 1) * (uint32_t)p.r;
+  uint32_t rank[RS];
+#pragma unroll
+  for (int s = 0; s < RS; ++s) rank[s] = 32 * s + 8 * g < p.r ? 32 * s + 8 * g : 0;
+  auto load_b = [&](int a, u32x4_t (&b)[RS]) {
+    const uint16_t *bm = reinterpret_cast<const uint16_t *>(p.B) + (int64_t)a * p.N * p.r;
+#pragma unroll
+    for (int s = 0; s < RS; ++s) b[s] = *reinterpret_cast<const u32x4_t *>(bm + brow + rank[s]);
+  };
+  const unsigned long long all = __ballot(l >= 0) & 0xFFFFull;
+  one4 base = {};
+  if (live && p.base) base = *reinterpret_cast<const one4 *>(reinterpret_cast<const one *>(p.base) + lr * p.ldb + c);
+  const float sc = l >= 0 && p.scaling ? p.scaling[l] : 1.0f;
+  u32x4_t b[RS] = {};
+  unsigned long long left = all;
+  int a = next_adapter(left, l);
+  if (a >= 0) load_b(a, b);  // on its way while h is formed
+  for (int now = a; now >= 0; now = next_adapter(left, l)) {
+    f32x4 acc[1][RB][1];
+    down_product<DT, RB, 1, kFewWaves, 1, kFewRing>(p, 0, &now, wave, (p.K + kStep - 1) / kStep,
+                                                    s_mem + wave * kFewRing, acc);
+    lds_barrier();  // the rings are read
+#pragma unroll
+    for (int i = 0; i < RB; ++i) s_acc[(wave * RB + i) * 64 + lane] = acc[0][i][0];
+    lds_barrier();
+    if (wave < RB) {
+      f32x4 v = s_acc[wave * 64 + lane];
+#pragma unroll
+      for (int w = 1; w < kFewWaves; ++w) v += s_acc[(w * RB + wave) * 64 + lane];
+      if (l == now) *reinterpret_cast<f32x4 *>(s_h + lr * kRow + 16 * wave + 4 * g) = v;
+    }
+    lds_barrier();  // before the rings are written again, and h is read
+  }
+  float h[RS][8];
+#pragma unroll
+  for (int s = 0; s < RS; ++s) {
+    const f32x4 *q = reinterpret_cast<const f32x4 *>(s_h + lr * kRow + rank[s]);
+    const f32x4 v[2] = {q[0], q[1]};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) h[s][e] = l >= 0 && 32 * s + 8 * g < p.r ? __fmul_rn(v[e / 4][e % 4], sc) : 0.f;
+  }
+  vec hi[RS], lo[RS];
+  const int ex = two_terms<DT, RS>(h, hi, lo);
+  f32x4 d = {0.f, 0.f, 0.f, 0.f};
+  left = all;
+  for (int now = next_adapter(left, l); now >= 0; now = next_adapter(left, l)) {
+    if (now != a) load_b(now, b);
+    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int s = 0; s < RS; ++s) {
+      const u32x4_t w = 32 * s + 8 * g < p.r ? b[s] : u32x4_t{0, 0, 0, 0};
+      acc = Half<DT>::mma(__builtin_bit_cast(vec, w), lo[s], acc);
+      acc = Half<DT>::mma(__builtin_bit_cast(vec, w), hi[s], acc);
+    }
+    if (l == now) d = acc;
+  }
+  if (!live) return;
+  one4 o = base;
+  if (l >= 0) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      o[e] = Half<DT>::round(__fadd_rn((float)base[e], DT == 1 ? __builtin_ldexpf(d[e], -ex) : d[e]));
+  }
+  *reinterpret_cast<one4 *>(reinterpret_cast<one *>(p.out) + lr * p.ldo + c) = o;
+}
+
 // Parts of K: enough workgroups to fill the card where tokens are few, a step a wave at least,
 // and no more parts than the second kernel adds up at ease.
 int split_count(int64_t T, int64_t K) {
@@ -570,6 +660,19 @@ int split_count(int64_t T, int64_t K) {
   int64_t s = 512 / tiles;
   if (s > steps / 4) s = steps / 4;
   return (int)(s < 1 ? 1 : s > kParts ? kParts : s);
+}
+
+// Whether the one kernel of few tokens is used: a single adapter of up to 2^17 values of A or up to
+// 4 of 2^16 together, and a compute unit for every workgroup. Measured in graphs, this kernel against the two (us; where
+// the host's launches are the bound, one launch saves 3.4 more):
+//   1 token: K 1024, N 1024, r 8 3.5, 6.1; K 4096, N 4096, r 16 5.2, 6.5, r 32 5.8, 6.6; N 32768,
+//   r 16 5.4, 6.5; K 8192, N 8192, r 16 7.3, 6.9; but K 14336, r 32 14.1, 7.9;
+//   4 tokens on 4 adapters: K 1024, r 8 5.6, 7.3; but K 4096, r 16 10.2, 7.7;
+//   16 tokens: 2 adapters, K 1024, r 8 4.9, 7.2; but K 4096, r 16 8.3, 7.7; 14 adapters, K 1024,
+//   r 8 20.0, 11.7.
+bool few(const AdapterArgs &a) {
+  const int64_t most = a.T < a.L ? a.T : a.L;
+  return a.T <= 16 && most <= 4 && most * a.r * a.K <= (most == 1 ? 1 << 17 : 1 << 16) && a.N <= 256 * kFewCols;
 }
 
 // The first kernel's waves and each one's ring of LDS: three steps of a single adapter's rows
@@ -611,6 +714,13 @@ hipError_t launch(AdapterArgs a, hipStream_t s) {
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     return launch_up<DT, RS, RS <= 2 ? 4 : 2, 1, true>(a, s);
+  }
+  if constexpr (RB <= 2) {
+    if (few(a)) {
+      hipLaunchKernelGGL((kq_adapter_few_kernel<DT, RB>), dim3((unsigned)((a.N + kFewCols - 1) / kFewCols)),
+                         dim3(kFewWaves * 64), 0, s, a);
+      return hipGetLastError();
+    }
   }
   // a decode batch's tile may have 16 adapters: workgroups share them out, up to some 1024
   const int64_t t16 = (a.T + 15) / 16;

@@ -306,3 +306,57 @@ def test_workspace_over_other_arguments_is_refused():
         assert _raw(ws=at) == B.KQ_ERR_INVALID_ARG, hex(at)
     # 4 tokens of 16 ranks in fp32, one part: 0x100 bytes, so its last 16 are the first of out
     assert _raw(ws=0x80000 - 0x100, out=0x80000 - 0x10) == B.KQ_ERR_INVALID_ARG
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("T,K,N,r,L", [(1, 64, 8, 8, 1), (1, 4096, 4096, 32, 64), (1, 8, 32768, 16, 2),
+                                       (1, 8, 32776, 16, 2), (4, 1032, 1000, 8, 9), (16, 2040, 136, 16, 4),
+                                       (16, 1000, 264, 32, 4), (3, 4104, 72, 8, 3), (16, 8192, 520, 8, 2),
+                                       (16, 1016, 136, 16, 4), (16, 512, 264, 32, 4), (2, 2048, 72, 16, 3)])
+def test_few_tokens(gpu, T, K, N, r, L, dtype):
+    for seed in range(2):
+        x, A, Bm, ad, base, s = _inputs(gpu, T, K, N, r, L, dtype, seed=seed)
+        _check(x, A, Bm, ad, base, s, B.adapter_add(x, A, Bm, ad, base=base, scaling=s))
+        none = ad.clone()
+        none[::2] = -1
+        _check(x, A, Bm, none, base, s, B.adapter_add(x, A, Bm, none, base=base, scaling=s, out=base.clone()))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [1, 5, 16])
+def test_few_tokens_that_are_not_finite(gpu, T):
+    """Infinities and NaN of one token, of one adapter, stay with the tokens that have them."""
+    import torch
+    x, A, Bm, ad, base, s = _inputs(gpu, T, 512, 264, 16, 4, "bf16", seed=T)
+    ad.copy_(torch.arange(T, device=ad.device) % 4 - 1)
+    want = B.adapter_add(x, A, Bm, ad, base=base, scaling=s)
+    A[2, 3, 7], Bm[2, 5, 1] = float("inf"), float("nan")
+    x2 = x.clone()
+    x2[T // 2, 9] = float("nan")
+    out = B.adapter_add(x2, A, Bm, ad, base=base, scaling=s)
+    touched = (ad == 2) | ((torch.arange(T, device=ad.device) == T // 2) & (ad >= 0))
+    assert torch.equal(out[~touched], want[~touched])
+    assert not torch.isfinite(out[touched]).all(1).any()
+
+
+@pytest.mark.gpu
+def test_few_tokens_in_a_graph(gpu):
+    import torch
+    x, A, Bm, ad, base, s = _inputs(gpu, 4, 1024, 1024, 16, 4, "fp16", seed=9)
+    out = torch.empty_like(base)
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        B.adapter_add(x, A, Bm, ad, base=base, scaling=s, out=out)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        B.adapter_add(x, A, Bm, ad, base=base, scaling=s, out=out)
+    for k in range(4):
+        x.copy_(torch.randn_like(x))
+        ad.copy_((ad + k) % 5 - 1)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = out.clone()
+        _check(x, A, Bm, ad, base, s, got)
+        assert torch.equal(got, B.adapter_add(x, A, Bm, ad, base=base, scaling=s))
