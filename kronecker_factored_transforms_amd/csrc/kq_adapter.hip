@@ -731,7 +731,13 @@ hipError_t launch(AdapterArgs a, hipStream_t s) {
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   constexpr int D = RB <= 2 ? 4 : RB <= 8 ? 2 : 1;
-  if (a.T < kJoin) return launch_up<DT, RS, RS <= 2 ? 4 : 2, D, false>(a, s);
+  if (a.T < kJoin) {
+    // 32 columns a wave where 64 leave the card half empty (us in a graph, 32 and 64 columns: 128
+    // tokens on 64 adapters, K = N = 4096, r 16 14.8, 16.6; 512 on 4 12.7, 13.1; but 256 on 64, N
+    // 14336 33.0, 32.4)
+    if (RS <= 2 && t16 * ((a.N + 255) / 256) <= 512) return launch_up<DT, RS, 2, D, false>(a, s);
+    return launch_up<DT, RS, RS <= 2 ? 4 : 2, D, false>(a, s);
+  }
   hipLaunchKernelGGL((kq_adapter_join_kernel<DT, RS>), dim3((unsigned)t16), dim3(64), 0, s, a);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
