@@ -6,11 +6,11 @@
 //
 // The groups' ends are read on the device (nothing waits for the host): a workgroup finds the
 // group and the row tile of its number by a scan of the groups' tile counts. The grid holds
-// one tile per kTile rows and one more per group, which is as many as ragged ends can make;
+// one tile per TILE rows and one more per group, which is as many as ragged ends can make;
 // the workgroups behind the last tile end at once.
 //
 // Few rows per group: bound by the weights' stream (64 experts of 4096 x 7168 INT4, 4 to 16 rows
-// each: 166-173 us, 5.5-5.7 TB/s). Many: by the matrix cores and what feeds them (16384 rows, 8
+// each: 162-166 us, 5.7-5.8 TB/s). Many: by the matrix cores and what feeds them (16384 rows, 8
 // experts, N 14336, K 4096: INT4 820-825 us, 2.34 POP/s; INT8 1000-1010 us, 1.9 POP/s; the
 // library's dense INT8 product of that size 848 us). INT4 spends 2.3 instructions a product on
 // unpacking; INT8 reads twice the bytes from LDS, whose writes and reads take as long as its
@@ -606,7 +606,7 @@ kq_status launch_tile(const GroupedArgs &a, hipStream_t s) {
 //     but R 8192, E 4, N 512, K 8192 INT8 (72 tiles of 256): 110 against 73; R 2048, E 64,
 //     N 4096, K 7168 INT4 (32 rows a group): 222 against 182;
 //   128 x 128 tiles otherwise; two workgroups of them share a compute unit. Up to 256 of them each
-//   has one to itself, and four steps in LDS: R 128, E 4, N 4096, K 4096 INT8 23.5 against 35.3,
+//   has one to itself, and four steps in LDS: R 128, E 4, N 4096, K 4096 INT8 22.3 against 35.3,
 //   R 2000, E 8, N 1024, K 2048 16.3 against 17.4 (INT4 within 3 %); but R 8192, E 4, N 512,
 //   K 8192 INT8 (272 tiles) 83 against 72.
 template <int BITS>
