@@ -179,13 +179,14 @@ __device__ __forceinline__ void mfma_piece(const u32x4_t &a, const u32x4_t &b, i
   }
 }
 
-// A workgroup: 16 MI output channels x 16 NI rows of one group; its waves split the reduction
-// (64 bytes of a row in turn) and add their parts up in LDS (integers: any order). Bound by the
-// weights' stream: the operands come straight from memory, and as many waves as fit keep their
-// loads going (8 of them a workgroup, one step each: 2 rows of 4096 x 4096 INT8 8.7 us, 4 waves
-// 10.3; 64 rows over 8 experts 26.9, with 4 steps of a wave in flight and fewer waves 30).
+// A workgroup: 16 MI output channels x 16 NI rows of one group; its waves split the reduction (U
+// steps of 64 bytes of a row in turn) and add their parts up in LDS (integers: any order). Bound by
+// the weights' stream: the operands come straight from memory, the weights of the next steps before
+// the products of these, and as many waves as fit keep their loads going (8 of them a workgroup: 2
+// rows of 4096 x 4096 INT8 8.7 us, 4 waves 10.3).
 template <int BITS, int MI, int NI, int WAVES>
 __global__ __launch_bounds__(WAVES * 64) void kq_grouped_stream_kernel(const GroupedArgs p, int tiles_m) {
+  constexpr int U = MI == 1 ? 2 : 1;
   __shared__ i32x4 s_acc[WAVES][MI * NI][64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int g = lane >> 4, lr = lane & 15;
@@ -201,6 +202,18 @@ __global__ __launch_bounds__(WAVES * 64) void kq_grouped_stream_kernel(const Gro
     const int64_t n = n0 + 16 * m + lr;
     wrow[m] = p.wq + tile.e * p.ldwe + (n < p.N ? n : p.N - 1) * p.ldwq + g * 16;
   }
+  // a row's last step may have fewer than 4 pieces, and a wave's last steps may lie behind it
+  auto in_row = [&](int s) { return s * 4 + g < p.pieces; };
+  auto load_a = [&](int s0, u32x4_t (&a)[U][MI]) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t o = in_row(s0 + u) ? (int64_t)(s0 + u) * 64 : -(int64_t)g * 16;
+#pragma unroll
+      for (int m = 0; m < MI; ++m) a[u][m] = *reinterpret_cast<const u32x4_t *>(wrow[m] + o);
+    }
+  };
+  u32x4_t a[U][MI];
+  load_a(wave * U, a);  // on their way before the rows' numbers are known
   int64_t src[NI];
 #pragma unroll
   for (int j = 0; j < NI; ++j) {
@@ -215,19 +228,26 @@ __global__ __launch_bounds__(WAVES * 64) void kq_grouped_stream_kernel(const Gro
   for (int m = 0; m < MI; ++m)
 #pragma unroll
     for (int j = 0; j < NI; ++j) acc[m][j] = i32x4{0, 0, 0, 0};
-  for (int s = wave; s * 4 < p.pieces; s += WAVES) {
-    const bool in = s * 4 + g < p.pieces;  // the last step may have fewer than 4 pieces
-    const int64_t o = in ? (int64_t)s * 64 : -(int64_t)g * 16;
-    const u32x4_t zero = {0, 0, 0, 0};
-    u32x4_t a[MI], b[NI];
+  const u32x4_t zero = {0, 0, 0, 0};
+  for (int s0 = wave * U; s0 * 4 < p.pieces; s0 += WAVES * U) {
+    u32x4_t b[U][NI], next[U][MI] = {};
 #pragma unroll
-    for (int m = 0; m < MI; ++m) a[m] = *reinterpret_cast<const u32x4_t *>(wrow[m] + o);
+    for (int u = 0; u < U; ++u) {
+      const int64_t o = in_row(s0 + u) ? (int64_t)(s0 + u) * 64 : -(int64_t)g * 16;
 #pragma unroll
-    for (int j = 0; j < NI; ++j) b[j] = *reinterpret_cast<const u32x4_t *>(xrow[j] + o);
+      for (int j = 0; j < NI; ++j) b[u][j] = *reinterpret_cast<const u32x4_t *>(xrow[j] + o);
+    }
+    if ((s0 + WAVES * U) * 4 < p.pieces) load_a(s0 + WAVES * U, next);
 #pragma unroll
-    for (int j = 0; j < NI; ++j)
+    for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int m = 0; m < MI; ++m) mfma_piece<BITS>(a[m], in ? b[j] : zero, acc[m][j]);
+      for (int j = 0; j < NI; ++j)
+#pragma unroll
+        for (int m = 0; m < MI; ++m) mfma_piece<BITS>(a[u][m], in_row(s0 + u) ? b[u][j] : zero, acc[m][j]);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int m = 0; m < MI; ++m) a[u][m] = next[u][m];
   }
 #pragma unroll
   for (int m = 0; m < MI; ++m)
@@ -566,15 +586,29 @@ __global__ __launch_bounds__((Tiling<BITS, SIDE>::kWaves * 64)) void kq_grouped_
   }
 }
 
-template <int BITS, int NI>
+template <int BITS, int MI, int NI>
 kq_status launch_stream(const GroupedArgs &a, hipStream_t s) {
-  constexpr int MI = 2, WAVES = 8;
+  constexpr int WAVES = 8;
   const int64_t tiles_m = (a.N + 16 * MI - 1) / (16 * MI);
   const int64_t tiles = a.R / (16 * NI) + (a.R < a.E ? a.R : a.E);
   if (tiles_m * tiles > 0x7FFFFFFF / (WAVES * 64)) return KQ_ERR_UNSUPPORTED;
   hipLaunchKernelGGL((kq_grouped_stream_kernel<BITS, MI, NI, WAVES>), dim3((unsigned)(tiles_m * tiles)),
                      dim3(WAVES * 64), 0, s, a, (int)tiles_m);
   return hipGetLastError() == hipSuccess ? KQ_OK : KQ_ERR_HIP;
+}
+
+// 16 channels a workgroup instead of 32 where INT8 weights of one or two rows a group stream by, or
+// where half a card has no workgroup (us, 16 against 32; weights from memory, and in brackets from
+// the last cache, where reading x twice as often costs more): 8 rows over 8 experts of 4096 x 4096
+// INT8 29.7, 32.7 (18.8, 16.4); 2 rows of 14336 x 4096 INT8 26.3, 29.6; 6 of 2048 x 7168 INT8 21.5,
+// 22.7 (17.6, 18.8); 32 rows over 4 experts, N 1024, INT8 7.8, 9.1 (8.8, 9.2), INT4 6.2, 7.0; but 64
+// rows over 8 experts INT8 33.6, 35.3 (34.0, 26.8); 8 over 8 INT4 19.2, 17.0; 2040 rows over 2, N 88,
+// K 8576 INT4 13.6, 10.8.
+template <int BITS, int NI>
+kq_status launch_stream(const GroupedArgs &a, int64_t groups, int64_t per_group, hipStream_t s) {
+  const int64_t tiles = (a.N + 31) / 32 * groups * ((per_group + 16 * NI - 1) / (16 * NI));
+  if ((BITS == 8 && per_group <= 2) || tiles <= 128) return launch_stream<BITS, 1, NI>(a, s);
+  return launch_stream<BITS, 2, NI>(a, s);
 }
 
 template <int BITS, int SIDE, int STAGES>
@@ -615,7 +649,8 @@ kq_status launch(const GroupedArgs &a, hipStream_t s) {
   const int64_t tiles128 = (a.N + 127) / 128 * (a.R / 128 + groups);
   const int64_t tiles256 = (a.N + 255) / 256 * (a.R / 256 + groups);
   if (tiles128 < 64 || (tiles128 < 512 && per_group <= 16))
-    return per_group <= 8 ? launch_stream<BITS, 1>(a, s) : launch_stream<BITS, 2>(a, s);
+    return per_group <= 8 ? launch_stream<BITS, 1>(a, groups, per_group, s)
+                          : launch_stream<BITS, 2>(a, groups, per_group, s);
   if (per_group >= 96 && tiles256 >= 192) return launch_tile<BITS, 256, 2>(a, s);
   return tiles128 <= 256 ? launch_tile<BITS, 128, 4>(a, s) : launch_tile<BITS, 128, 2>(a, s);
 }
