@@ -11,7 +11,7 @@
 //
 // Few rows per group: bound by the weights' stream (64 experts of 4096 x 7168 INT4, 4 to 16 rows
 // each: 162-166 us, 5.7-5.8 TB/s). Many: by the matrix cores and what feeds them (16384 rows, 8
-// experts, N 14336, K 4096: INT4 820-825 us, 2.34 POP/s; INT8 1000-1010 us, 1.9 POP/s; the
+// experts, N 14336, K 4096: INT4 815-830 us, 2.3-2.36 POP/s; INT8 996-1010 us, 1.9 POP/s; the
 // library's dense INT8 product of that size 848 us). INT4 spends 2.3 instructions a product on
 // unpacking; INT8 reads twice the bytes from LDS, whose writes and reads take as long as its
 // products.
@@ -320,27 +320,40 @@ struct Tiling : Share<BITS, SIDE> {
   static constexpr int kMI = SIDE / S::kWM / S::kSide, kApart = S::kWN * S::kSide, kBlocks = SIDE / kApart;
   static constexpr int kOpBytes = SIDE * kStep;  // per operand and step in LDS
   static constexpr int kOutBytes = 2 * kApart * (SIDE * 4 + 16);  // two blocks of fp32 output rows
+  // Weights come from memory, rows of x from the caches: an INT8 tile of 256 that is not full, and so
+  // waits for its weights rather than for its products, has them a step further ahead than x (3062
+  // rows over 16 experts, N 11008, K 4096 220 us, 229 without; full tiles are slower with it, 16384
+  // rows over 8 experts, N 14336, K 4096 1030, 996, and so is INT4)
+  static constexpr bool kFar = BITS == 8 && SIDE == 256;
   template <int STAGES>
-  static constexpr int kLds = STAGES * 2 * kOpBytes > kOutBytes ? STAGES * 2 * kOpBytes : kOutBytes;
+  static constexpr int kInts = (2 * STAGES + (kFar ? 1 : 0)) * kOpBytes;
+  template <int STAGES>
+  static constexpr int kLds = kInts<STAGES> > kOutBytes + SIDE ? kInts<STAGES> : kOutBytes + SIDE;
   static constexpr int kLoads = kOpBytes / 1024 / kWaves;
   static_assert(kLoads * 1024 * kWaves == kOpBytes, "the tile splits evenly over the waves");
 };
 
-// Wait until at most min(left, MOST) later steps of LOADS loads each are still on their way
-template <int LOADS, int MOST>
-__device__ __forceinline__ void wait_steps(int left) {
-  static_assert(LOADS * MOST < 64, "fits the wait counter");
-  if constexpr (MOST == 0) {
+// Wait until a step's operands have landed, `left` steps before the last one, where the loads of up
+// to MOST pairs (x of a step, W of the step MORE behind it) may still be on their way behind them:
+// those pairs' and, with MORE, the weights that came with the step's own x.
+template <int W, int X, int MORE, int MOST>
+__device__ __forceinline__ void wait_pairs(int left) {
+  static_assert(MORE * W + (W + X) * MOST < 64, "fits the wait counter");
+  static_assert(MORE <= 1, "the weights one step ahead of x, or none");
+  if (left >= MOST + MORE) {
+    wait_and_fence<wait_vm_imm(MORE * W + (W + X) * MOST)>();
+  } else if constexpr (MOST == 0) {
     wait_and_fence<kWaitVm0>();
+  } else if (MORE && left == MOST) {  // the last pair has no weights
+    wait_and_fence<wait_vm_imm((W + X) * MOST)>();
   } else {
-    if (left >= MOST) wait_and_fence<wait_vm_imm(LOADS * MOST)>();
-    else wait_steps<LOADS, MOST - 1>(left);
+    wait_pairs<W, X, MORE, MOST - 1>(left);
   }
 }
 
 template <int BITS, int SIDE, int STAGES, int OUT, int NU>
 __device__ __forceinline__ void tile_product(const GroupedArgs &p, const RowTile &tile, int64_t n0,
-                                             unsigned char *s_buf, unsigned char *s_ok) {
+                                             unsigned char *s_buf) {
   typedef Tiling<BITS, SIDE> S;
   typedef typename S::acc_t acc_t;
   constexpr int kOpBytes = S::kOpBytes, kLoads = S::kLoads, kXLoads = kLoads * NU / S::kBlocks;
@@ -350,7 +363,10 @@ __device__ __forceinline__ void tile_product(const GroupedArgs &p, const RowTile
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int g = lane / S::kSide, lr = lane % S::kSide;
   const int wm = wave % S::kWM, wn = wave / S::kWM;
-  auto buf = [&](int b) { return s_buf + b * 2 * kOpBytes; };  // weight rows, then the tile's rows
+  constexpr int kMore = S::kFar && NU < S::kBlocks ? 1 : 0, kWStages = STAGES + kMore;
+  auto w_place = [&](int b) { return s_buf + b * kOpBytes; };
+  auto x_place = [&](int b) { return s_buf + (kWStages + b) * kOpBytes; };
+  auto plus = [](int b, int n, int places) { return b + n < places ? b + n : b + n - places; };
 
   // DMA: instruction J = wave kLoads + j of an operand fills kRowsPer tile rows; a lane lands
   // at position lane % kChunks of row R and reads piece (lane % kChunks) ^ swz(R) of that row,
@@ -377,27 +393,48 @@ __device__ __forceinline__ void tile_product(const GroupedArgs &p, const RowTile
     ax[j] = p.xq + t * p.ldxq + piece_of(kXLoads, j) * 16;
   }
   const int steps = (p.pieces + kChunks - 1) / kChunks;
-  auto dma_step = [&](int ks, int b) {
-    unsigned char *w_to = buf(b) + wave * (kLoads * 1024);
-    unsigned char *x_to = buf(b) + kOpBytes + wave * (kXLoads * 1024);
-    const uint8_t *w = wbase + (int64_t)ks * kStep;
-    if ((ks + 1) * kChunks <= p.pieces) {
+  // One load of step s, whole (inside the row for all lanes), or ending in it: the rest comes from a
+  // block of zeros. Steps come in order, and x's addresses move along.
+  auto load_w = [&](int s, int b, int j, bool whole) {
+    unsigned char *to = w_place(b) + (wave * kLoads + j) * 1024;
+    const uint8_t *w = wbase + (int64_t)s * kStep;
+    if (whole) dma16<false>(w, vw[j], lds_addr(to));
+    else dma16_addr<false>(s * kChunks + piece_of(kLoads, j) < p.pieces ? w + vw[j] : kZeros, lds_addr(to));
+  };
+  auto load_x = [&](int s, int b, int j, bool whole) {
+    unsigned char *to = x_place(b) + (wave * kXLoads + j) * 1024;
+    dma16_addr<false>(whole || s * kChunks + piece_of(kXLoads, j) < p.pieces ? ax[j] : kZeros, lds_addr(to));
+    ax[j] += kStep;
+  };
+  // x of step s and the weights of step s + kMore; the weights that are further ahead go last, so
+  // that a wait for x leaves them on their way
+  auto load_pair = [&](int s, int bx, int bw) {
+    if ((s + kMore + 1) * kChunks <= p.pieces) {
+      if constexpr (kMore == 0) {
 #pragma unroll
-      for (int j = 0; j < kLoads; ++j) {
-        dma16<false>(w, vw[j], lds_addr(w_to + j * 1024));
-        if (j < kXLoads) {
-          dma16_addr<false>(ax[j], lds_addr(x_to + j * 1024));
-          ax[j] += kStep;
+        for (int j = 0; j < kLoads; ++j) {
+          load_w(s, bw, j, true);
+          if (j < kXLoads) load_x(s, bx, j, true);
         }
+      } else {
+#pragma unroll
+        for (int j = 0; j < kXLoads; ++j) load_x(s, bx, j, true);
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j) load_w(s + kMore, bw, j, true);
       }
-    } else {  // the last step of a row that ends inside it: the rest comes from a block of zeros
+    } else {
+      if (s < steps)
 #pragma unroll
-      for (int j = 0; j < kLoads; ++j)
-        dma16_addr<false>(ks * kChunks + piece_of(kLoads, j) < p.pieces ? w + vw[j] : kZeros, lds_addr(w_to + j * 1024));
+        for (int j = 0; j < kXLoads; ++j) load_x(s, bx, j, false);
+      if (s + kMore < steps)
 #pragma unroll
-      for (int j = 0; j < kXLoads; ++j)
-        dma16_addr<false>(ks * kChunks + piece_of(kXLoads, j) < p.pieces ? ax[j] : kZeros, lds_addr(x_to + j * 1024));
+        for (int j = 0; j < kLoads; ++j) load_w(s + kMore, bw, j, false);
     }
+  };
+  auto load_first = [&]() {  // the weights of the steps that no pair has
+    if constexpr (kMore == 1)
+#pragma unroll
+      for (int j = 0; j < kLoads; ++j) load_w(0, 0, j, kChunks <= p.pieces);
   };
 
   acc_t acc[S::kMI][NU];
@@ -414,6 +451,7 @@ __device__ __forceinline__ void tile_product(const GroupedArgs &p, const RowTile
   // The steps of this lane's rows, and which of them are written: loaded here, so that the
   // epilogue does not wait for them (a row's number, then its step) row by row.
   float sx[NU];
+  bool written[NU];
 #pragma unroll
   for (int i = 0; i < NU; ++i) {
     const int R = row_x + i * S::kApart;
@@ -421,7 +459,7 @@ __device__ __forceinline__ void tile_product(const GroupedArgs &p, const RowTile
     if (p.rows) t = p.rows[t];
     const bool in = t >= 0 && t < p.T;
     sx[i] = load_step(p.sx, in ? t : 0, p.scale_fp16);
-    if (wm == 0 && g == 0) s_ok[R] = R < tile.count && in;  // read behind the reduction's barriers
+    written[i] = R < tile.count && in;
   }
 
   // A step's fragments come in kParts parts, each read while the part before it multiplies;
@@ -430,7 +468,8 @@ __device__ __forceinline__ void tile_product(const GroupedArgs &p, const RowTile
   struct Part {
     u32x4_t w[S::kMI], x[NU];
   };
-  auto read_part = [&](const unsigned char *w, int q) {
+  auto read_part = [&](int bw, int bx, int q) {
+    const unsigned char *w = w_place(bw), *x = x_place(bx);
     Part f;
     const int off = ((64 / S::kSide * q + g) ^ sl) * 16;
 #pragma unroll
@@ -438,7 +477,7 @@ __device__ __forceinline__ void tile_product(const GroupedArgs &p, const RowTile
       f.w[m] = *reinterpret_cast<const u32x4_t *>(w + (row_w + m * S::kSide) * kStep + off);
 #pragma unroll
     for (int i = 0; i < NU; ++i)
-      f.x[i] = *reinterpret_cast<const u32x4_t *>(w + kOpBytes + (row_x + i * S::kApart) * kStep + off);
+      f.x[i] = *reinterpret_cast<const u32x4_t *>(x + (row_x + i * S::kApart) * kStep + off);
     return f;
   };
   auto multiply = [&](const Part &f) {
@@ -476,51 +515,53 @@ __device__ __forceinline__ void tile_product(const GroupedArgs &p, const RowTile
     // the unpacking between reads and products covers the reads; a second part in registers costs
     // more than it gives (256: it spills, 2042 against 841 us; 128: 67 against 63 us on R 8192,
     // N 512, K 8192)
+    load_first();
 #pragma unroll
-    for (int k = 0; k < STAGES - 1; ++k)
-      if (k < steps) dma_step(k, k);
-    int b = 0;  // this step's buffer
+    for (int k = 0; k < STAGES - 1; ++k) load_pair(k, k, k + kMore);
+    int bw = 0, bx = 0;  // this step's places
     for (int ks = 0; ks < steps; ++ks) {
-      wait_steps<kLoads + kXLoads, STAGES - 2>(steps - 1 - ks);
+      wait_pairs<kLoads, kXLoads, kMore, STAGES - 2>(steps - 1 - ks);
       sync();  // this step has landed for every wave, and every wave is done with the one before
-      if (ks + STAGES - 1 < steps) dma_step(ks + STAGES - 1, b == 0 ? STAGES - 1 : b - 1);
+      load_pair(ks + STAGES - 1, plus(bx, STAGES - 1, STAGES), plus(bw, kWStages - 1, kWStages));
 #pragma unroll
-      for (int q = 0; q < kParts; ++q) multiply(read_part(buf(b), q));
+      for (int q = 0; q < kParts; ++q) multiply(read_part(bw, bx, q));
       wait_and_fence<kWaitLgkm0>();
-      b = b + 1 == STAGES ? 0 : b + 1;
+      bw = plus(bw, 1, kWStages);
+      bx = plus(bx, 1, STAGES);
     }
   } else {
     // each part is read while the one before it multiplies, across the steps
+    load_first();
 #pragma unroll
-    for (int k = 0; k < STAGES; ++k)
-      if (k < steps) dma_step(k, k);
-    wait_steps<kLoads + kXLoads, STAGES - 1>(steps - 1);
+    for (int k = 0; k < STAGES; ++k) load_pair(k, k, k + kMore);
+    wait_pairs<kLoads, kXLoads, kMore, STAGES - 1>(steps - 1);
     sync();
-    Part f = read_part(buf(0), 0);
-    int b = 0;  // this step's buffer
+    Part f = read_part(0, 0, 0);
+    int bw = 0, bx = 0;  // this step's places
     for (int ks = 0; ks < steps; ++ks) {
-      const int after = b + 1 == STAGES ? 0 : b + 1;
+      const int w_after = plus(bw, 1, kWStages), x_after = plus(bx, 1, STAGES);
 #pragma unroll
       for (int q = 0; q < kParts; ++q) {
         Part next = f;
         if (q + 1 < kParts) {
-          next = read_part(buf(b), q + 1);
+          next = read_part(bw, bx, q + 1);
         } else if (ks + 1 < steps) {
-          // this wave's reads of buffer b have returned, and its loads of the next step have
-          // landed; behind the barrier that holds for every wave, so b may be overwritten and
-          // the next buffer read
+          // this wave's reads of this step have returned, and its loads of the next step have
+          // landed; behind the barrier that holds for every wave, so this step's places may be
+          // overwritten and the next ones read
           wait_and_fence<kWaitLgkm0>();
-          wait_steps<kLoads + kXLoads, STAGES - 2>(steps - 2 - ks);
+          wait_pairs<kLoads, kXLoads, kMore, STAGES - 2>(steps - 2 - ks);
           sync();
-          next = read_part(buf(after), 0);
-          if (ks + STAGES < steps) dma_step(ks + STAGES, b);
+          next = read_part(w_after, x_after, 0);
+          load_pair(ks + STAGES, bx, bw);
         }
         __builtin_amdgcn_sched_barrier(0);
         multiply(f);
         __builtin_amdgcn_sched_barrier(0);
         f = next;
       }
-      b = after;
+      bw = w_after;
+      bx = x_after;
     }
   }
 
@@ -531,7 +572,7 @@ __device__ __forceinline__ void tile_product(const GroupedArgs &p, const RowTile
   constexpr int kQ = S::kMI * kRegs / 4;  // groups of 4 channels
   constexpr int kSize = OUT == KQ_FP32 ? 4 : 2, kRowBytes = SIDE * kSize + 16;
   constexpr int kRowLanes = SIDE * kSize / 16, kAtOnce = 64 / kRowLanes, kPer = 16 / kSize;
-  static_assert(2 * S::kApart * kRowBytes <= S::template kLds<STAGES>, "two places of rows");
+  static_assert(2 * S::kApart * kRowBytes <= S::kOutBytes, "two places of rows");
   const int ml = wm * (SIDE / S::kWM) + 4 * g;  // this lane's channels: ml + group_at(q)
   auto group_at = [](int q) { return q / (kRegs / 4) * S::kSide + q % (kRegs / 4) * 4 * (64 / S::kSide); };
   float sw[kQ][4];
@@ -539,6 +580,10 @@ __device__ __forceinline__ void tile_product(const GroupedArgs &p, const RowTile
   const int64_t nc = n0 + lane % kRowLanes * kPer;  // the channels this lane stores
   wait_and_fence<kWaitLgkm0>();
   sync();  // every wave has read the last step
+  unsigned char *s_ok = s_buf + S::kOutBytes;  // which rows of the tile are written
+#pragma unroll
+  for (int i = 0; i < NU; ++i)
+    if (wm == 0 && g == 0) s_ok[row_x + i * S::kApart] = written[i];
 #pragma unroll
   for (int i = 0; i < NU; ++i) {
     unsigned char *rows = s_buf + (i & 1) * (S::kApart * kRowBytes);
@@ -552,9 +597,9 @@ __device__ __forceinline__ void tile_product(const GroupedArgs &p, const RowTile
       }
       store_out4<OUT>(rows + row_x * kRowBytes, ml + group_at(q), v, 4);
     }
-    const unsigned long long ok = __ballot(lane < S::kApart && s_ok[i * S::kApart + lane % S::kApart]);
     wait_and_fence<kWaitLgkm0>();
     sync();
+    const unsigned long long ok = __ballot(lane < S::kApart && s_ok[i * S::kApart + lane % S::kApart]);
 #pragma unroll
     for (int k = 0; k < S::kApart / (kAtOnce * S::kWaves); ++k) {
       const int r = (k * S::kWaves + wave) * kAtOnce + lane / kRowLanes;
@@ -570,19 +615,18 @@ template <int BITS, int SIDE, int STAGES, int OUT>
 __global__ __launch_bounds__((Tiling<BITS, SIDE>::kWaves * 64)) void kq_grouped_tile_kernel(const GroupedArgs p, int tiles_m) {
   typedef Tiling<BITS, SIDE> S;
   __shared__ __align__(16) unsigned char s_buf[S::template kLds<STAGES>];
-  __shared__ unsigned char s_ok[SIDE];  // which rows of the tile are written
   const RowTile tile = find_tile<SIDE>(p.offsets, p.E, p.R, (int)(blockIdx.x / tiles_m));
   if (tile.e < 0) return;
   const int64_t n0 = (int64_t)(blockIdx.x % tiles_m) * SIDE;
   if constexpr (S::kBlocks == 4) {
-    if (tile.count > 3 * S::kApart) tile_product<BITS, SIDE, STAGES, OUT, 4>(p, tile, n0, s_buf, s_ok);
-    else if (tile.count > 2 * S::kApart) tile_product<BITS, SIDE, STAGES, OUT, 3>(p, tile, n0, s_buf, s_ok);
-    else if (tile.count > S::kApart) tile_product<BITS, SIDE, STAGES, OUT, 2>(p, tile, n0, s_buf, s_ok);
-    else tile_product<BITS, SIDE, STAGES, OUT, 1>(p, tile, n0, s_buf, s_ok);
+    if (tile.count > 3 * S::kApart) tile_product<BITS, SIDE, STAGES, OUT, 4>(p, tile, n0, s_buf);
+    else if (tile.count > 2 * S::kApart) tile_product<BITS, SIDE, STAGES, OUT, 3>(p, tile, n0, s_buf);
+    else if (tile.count > S::kApart) tile_product<BITS, SIDE, STAGES, OUT, 2>(p, tile, n0, s_buf);
+    else tile_product<BITS, SIDE, STAGES, OUT, 1>(p, tile, n0, s_buf);
   } else {
     static_assert(S::kBlocks == 2, "blocks of a wave");
-    if (tile.count > S::kApart) tile_product<BITS, SIDE, STAGES, OUT, 2>(p, tile, n0, s_buf, s_ok);
-    else tile_product<BITS, SIDE, STAGES, OUT, 1>(p, tile, n0, s_buf, s_ok);
+    if (tile.count > S::kApart) tile_product<BITS, SIDE, STAGES, OUT, 2>(p, tile, n0, s_buf);
+    else tile_product<BITS, SIDE, STAGES, OUT, 1>(p, tile, n0, s_buf);
   }
 }
 
