@@ -641,17 +641,19 @@ kq_status launch_stream(const GroupedArgs &a, hipStream_t s) {
   return hipGetLastError() == hipSuccess ? KQ_OK : KQ_ERR_HIP;
 }
 
-// 16 channels a workgroup instead of 32 where INT8 weights of one or two rows a group stream by, or
-// where half a card has no workgroup (us, 16 against 32; weights from memory, and in brackets from
-// the last cache, where reading x twice as often costs more): 8 rows over 8 experts of 4096 x 4096
-// INT8 29.7, 32.7 (18.8, 16.4); 2 rows of 14336 x 4096 INT8 26.3, 29.6; 6 of 2048 x 7168 INT8 21.5,
-// 22.7 (17.6, 18.8); 32 rows over 4 experts, N 1024, INT8 7.8, 9.1 (8.8, 9.2), INT4 6.2, 7.0; but 64
-// rows over 8 experts INT8 33.6, 35.3 (34.0, 26.8); 8 over 8 INT4 19.2, 17.0; 2040 rows over 2, N 88,
-// K 8576 INT4 13.6, 10.8.
+// 16 channels a workgroup instead of 32 where many INT8 weights of one or two rows a group stream
+// by, or where half a card has no workgroup (us, 16 against 32; weights from memory, and in brackets
+// from the last cache, where reading x twice as often costs more):
+//   8 rows over 8 experts of 4096 x 4096 INT8 29.7, 32.7 (18.8, 16.4); 2 rows of 14336 x 4096 INT8
+//   26.3, 29.6; 6 of 2048 x 7168 INT8 21.5, 22.7 (17.6, 18.8); but 2 of 4096 x 4096 INT8 (256
+//   workgroups of 32) 12.0, 10.8; 64 rows over 8 experts 33.6, 35.3 (34.0, 26.8); 8 over 8 INT4 19.2,
+//   17.0;
+//   32 rows over 4 experts, N 1024, INT8 7.8, 9.1 (8.8, 9.2), INT4 6.2, 7.0; but 2040 rows over 2, N
+//   88, K 8576 INT4 (192 workgroups of 32) 13.6, 10.8.
 template <int BITS, int NI>
 kq_status launch_stream(const GroupedArgs &a, int64_t groups, int64_t per_group, hipStream_t s) {
   const int64_t tiles = (a.N + 31) / 32 * groups * ((per_group + 16 * NI - 1) / (16 * NI));
-  if ((BITS == 8 && per_group <= 2) || tiles <= 128) return launch_stream<BITS, 1, NI>(a, s);
+  if ((BITS == 8 && per_group <= 2 && tiles > 256) || tiles <= 128) return launch_stream<BITS, 1, NI>(a, s);
   return launch_stream<BITS, 2, NI>(a, s);
 }
 
